@@ -33,6 +33,8 @@ EXPORTED = (
     "moe_routing_stats", "moe_workspace_routing", "moe_commit_blocks", "moe_plan_widths",
     "moe_substitute", "moe_lynx_remap", "moe_page_reload", "moe_page_commit",
     "moe_page_offload",
+    "moe_permute_tokens", "moe_permute_tokens_backward", "moe_unpermute_tokens",
+    "moe_unpermute_tokens_backward", "moe_fp8_quantize", "moe_fp8_quantize_silu", "moe_fp8_gemm",
     "moe_last_error",
 )
 
@@ -68,6 +70,7 @@ def _load():
                           "(hipcc --offload-arch=gfx950); there is no CPU fallback")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, Z, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p
+    L = ctypes.c_int64
     sig = {
         "moe_route_topk": ([P, I, I, I, P, P, S], I),
         "moe_group_by_expert": ([P, I, I, I, P, P, P, P, P, Z, S], I),
@@ -91,6 +94,13 @@ def _load():
         "moe_substitute": ([P, I, I, I, P, I, ctypes.c_float, P, P, P, P, P, ctypes.c_float, P, S], I),
         "moe_lynx_remap": ([P, I, I, I, ctypes.c_float, P, P, P, S], I),
         "moe_plan_widths": ([I, P, P, P, P, P, P, ctypes.c_int64, P, P], I),
+        "moe_permute_tokens": ([P, I, L, I, I, I, I, P, P, P, P, L, P, S], I),
+        "moe_permute_tokens_backward": ([P, I, L, I, I, I, P, P, L, S], I),
+        "moe_unpermute_tokens": ([P, I, L, I, I, I, P, P, P, L, P, L, S], I),
+        "moe_unpermute_tokens_backward": ([P, I, L, P, L, I, I, I, P, P, P, L, P, S], I),
+        "moe_fp8_quantize": ([P, I, L, I, I, P, P, L, P, S], I),
+        "moe_fp8_quantize_silu": ([P, I, L, I, I, P, P, L, P, S], I),
+        "moe_fp8_gemm": ([P, L, P, I, P, P, I, I, I, I, P, P, I, P, I, L, S], I),
         "moe_last_error": ([], ctypes.c_char_p),
     }
     for name, (args, res) in sig.items():
@@ -365,6 +375,204 @@ def moe_profile_stop(max_kernels: int = 32) -> dict:
         name = raw[64 * i: 64 * i + 64].split(b"\0", 1)[0].decode()
         out[name] = (ms[i], cnt[i])
     return out
+
+
+# ---------------------------------------------------------------------------------------------
+# Row operators: tokens sorted by expert and back, e4m3 quantising, the grouped e4m3 product
+# ---------------------------------------------------------------------------------------------
+MOE_DTYPE_F16, MOE_DTYPE_BF16, MOE_DTYPE_F32 = 0, 1, 2
+MOE_FP8_BLOCK = 128
+_row_types = {}   # torch dtype -> MOE_DTYPE_* of row elements, and torch's own names; filled at the first call
+
+
+def _types():
+    if not _row_types:
+        import torch
+        _row_types.update({torch.float16: MOE_DTYPE_F16, torch.bfloat16: MOE_DTYPE_BF16,
+                           torch.float32: MOE_DTYPE_F32, "i32": torch.int32, "f32": torch.float32,
+                           "e4m3": (torch.float8_e4m3fn, torch.uint8),
+                           "device": torch.cuda.current_device, "on": torch.cuda.device,
+                           "stream": torch._C._cuda_getCurrentRawStream})
+    return _row_types
+
+
+def _bad(fn: str, msg: str) -> MoeError:
+    return MoeError(fn, MOE_EINVAL, msg)
+
+
+def _rows(fn: str, name: str, t, rows: int, cols: int, dtype, device) -> int:
+    """Check a [rows, cols] tensor with contiguous rows; returns its row stride in elements."""
+    if t.dtype is not dtype and t.dtype != dtype:
+        raise _bad(fn, f"{name} is {t.dtype}, not {dtype}")
+    if t.device != device:
+        raise _bad(fn, f"{name} is on {t.device}, not {device}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise _bad(fn, f"{name} has shape {tuple(t.shape)}, not {(rows, cols)}")
+    step, one = t.stride()
+    if one != 1 and cols > 1:
+        raise _bad(fn, f"{name} needs contiguous rows (strides {t.stride()})")
+    return step if rows > 1 else max(step, cols)
+
+
+def _flat(fn: str, name: str, t, numel: int, dtype, device) -> int:
+    """Check a contiguous tensor of `numel` elements; returns its address."""
+    if t.dtype != dtype:
+        raise _bad(fn, f"{name} is {t.dtype}, not {dtype}")
+    if t.device != device:
+        raise _bad(fn, f"{name} is on {t.device}, not {device}")
+    if t.numel() != numel or not t.is_contiguous():
+        raise _bad(fn, f"{name} needs {numel} contiguous elements (shape {tuple(t.shape)}, strides {t.stride()})")
+    return t.data_ptr()
+
+
+def _row_dtype(fn: str, name: str, t) -> int:
+    ty = _types()
+    code = ty.get(t.dtype)
+    if code is None:
+        raise _bad(fn, f"{name} is {t.dtype}: rows are float16, bfloat16 or float32")
+    if not t.is_cuda:
+        raise _bad(fn, f"{name} is on {t.device}, not on a GPU")
+    if t.dim() != 2:
+        raise _bad(fn, f"{name} has shape {tuple(t.shape)}: rows are two-dimensional")
+    return code
+
+
+def _run_on(fn: str, device, stream, *args) -> None:
+    """Call `fn` with the device of its tensors current, on `stream` or that device's current one."""
+    ty = _types()
+    index = device.index
+    call = getattr(_lib, fn)
+    if stream is None:
+        handle = ty["stream"](index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if index == ty["device"]():
+        rc = call(*args, handle)
+    else:
+        with ty["on"](index):
+            rc = call(*args, handle)
+    if rc != MOE_OK:
+        _check(fn, rc)
+
+
+def moe_permute_tokens(x, topk_ids, expert_offsets, sorted_pairs, x_sorted, pair_rows, stream=None) -> None:
+    """x_sorted[i] = x[sorted_pairs[i] // k] for the placed pairs of moe_group_by_expert's output
+    (rows behind them are left alone), and pair_rows int32 [T, k], the row of each pair or -1.
+    x [T, H] and x_sorted [T*k, H] fp16, bf16 or fp32 with contiguous rows."""
+    fn = "moe_permute_tokens"
+    code, dev, i32 = _row_dtype(fn, "x", x), x.device, _types()["i32"]
+    T, H = x.shape
+    k = topk_ids.shape[1] if topk_ids.dim() == 2 else topk_ids.numel() // max(T, 1)
+    n = T * k
+    _run_on(fn, dev, stream, x.data_ptr(), code, _rows(fn, "x", x, T, H, x.dtype, dev), T, k,
+            expert_offsets.numel() - 1, H, _flat(fn, "topk_ids", topk_ids, n, i32, dev),
+            _flat(fn, "expert_offsets", expert_offsets, expert_offsets.numel(), i32, dev),
+            _flat(fn, "sorted_pairs", sorted_pairs, n, i32, dev), x_sorted.data_ptr(),
+            _rows(fn, "x_sorted", x_sorted, n, H, x.dtype, dev), _flat(fn, "pair_rows", pair_rows, n, i32, dev))
+
+
+def moe_permute_tokens_backward(dx_sorted, pair_rows, dx, stream=None) -> None:
+    """dx[t] = sum of dx_sorted's rows of token t's pairs (pair_rows int32 [T, k]; -1: no row)."""
+    fn = "moe_permute_tokens_backward"
+    code, dev = _row_dtype(fn, "dx", dx), dx.device
+    T, H = dx.shape
+    n = pair_rows.numel()
+    _run_on(fn, dev, stream, dx_sorted.data_ptr(), code, _rows(fn, "dx_sorted", dx_sorted, n, H, dx.dtype, dev), T,
+            _slots(fn, pair_rows, T), H, _flat(fn, "pair_rows", pair_rows, n, _types()["i32"], dev), dx.data_ptr(),
+            _rows(fn, "dx", dx, T, H, dx.dtype, dev))
+
+
+def _slots(fn: str, pair_rows, T: int) -> int:
+    if pair_rows.dim() != 2 or pair_rows.shape[0] != T:
+        raise _bad(fn, f"pair_rows has shape {tuple(pair_rows.shape)}, not ({T}, k)")
+    return pair_rows.shape[1]
+
+
+def moe_unpermute_tokens(y_sorted, pair_rows, gates, y, add=None, stream=None) -> None:
+    """y[t] = sum_j gates[t, j] * y_sorted[pair_rows[t, j]] (+ add[t]); gates fp32 [T, k] or None (1)."""
+    fn = "moe_unpermute_tokens"
+    code, dev, ty = _row_dtype(fn, "y", y), y.device, _types()
+    T, H = y.shape
+    n = pair_rows.numel()
+    _run_on(fn, dev, stream, y_sorted.data_ptr(), code, _rows(fn, "y_sorted", y_sorted, n, H, y.dtype, dev), T,
+            _slots(fn, pair_rows, T), H, _flat(fn, "pair_rows", pair_rows, n, ty["i32"], dev),
+            None if gates is None else _flat(fn, "gates", gates, n, ty["f32"], dev),
+            None if add is None else add.data_ptr(), 0 if add is None else _rows(fn, "add", add, T, H, y.dtype, dev),
+            y.data_ptr(), _rows(fn, "y", y, T, H, y.dtype, dev))
+
+
+def moe_unpermute_tokens_backward(dy, y_sorted, pair_rows, gates, dy_sorted, dgates, stream=None) -> None:
+    """dy_sorted[pair_rows[t, j]] = gates[t, j] * dy[t] and dgates[t, j] = <dy[t], y_sorted[pair_rows[t, j]]>
+    (0 without a row).  dy_sorted or dgates may be None; y_sorted may be None when dgates is."""
+    fn = "moe_unpermute_tokens_backward"
+    code, dev, ty = _row_dtype(fn, "dy", dy), dy.device, _types()
+    T, H = dy.shape
+    n = pair_rows.numel()
+
+    def rows(name, t):
+        return (None, 0) if t is None else (t.data_ptr(), _rows(fn, name, t, n, H, dy.dtype, dev))
+
+    _run_on(fn, dev, stream, dy.data_ptr(), code, _rows(fn, "dy", dy, T, H, dy.dtype, dev), *rows("y_sorted", y_sorted),
+            T, _slots(fn, pair_rows, T), H, _flat(fn, "pair_rows", pair_rows, n, ty["i32"], dev),
+            None if gates is None else _flat(fn, "gates", gates, n, ty["f32"], dev), *rows("dy_sorted", dy_sorted),
+            None if dgates is None else _flat(fn, "dgates", dgates, n, ty["f32"], dev))
+
+
+def _e4m3(fn: str, name: str, t, device):
+    if t.dtype not in _types()["e4m3"]:
+        raise _bad(fn, f"{name} is {t.dtype}, not float8_e4m3fn (or uint8 holding it)")
+    if t.device != device:
+        raise _bad(fn, f"{name} is on {t.device}, not {device}")
+
+
+def _quantize(fn: str, x, K: int, q, scales, n_rows, stream) -> None:
+    code, dev, ty = _row_dtype(fn, "x", x), x.device, _types()
+    M, cols = x.shape
+    _e4m3(fn, "q", q, dev)
+    _run_on(fn, dev, stream, x.data_ptr(), code, _rows(fn, "x", x, M, cols, x.dtype, dev), M, K,
+            None if n_rows is None else _flat(fn, "n_rows", n_rows, 1, ty["i32"], dev), q.data_ptr(),
+            _rows(fn, "q", q, M, K, q.dtype, dev),
+            _flat(fn, "scales", scales, M * -(-K // MOE_FP8_BLOCK), ty["f32"], dev))
+
+
+def moe_fp8_quantize(x, q, scales, n_rows=None, stream=None) -> None:
+    """x [M, K] -> q e4m3 [M, K] and scales fp32 [M, ceil(K/128)], one for each 128 columns of a
+    row.  n_rows: optional device int32 [1]; rows from it on are left alone."""
+    _quantize("moe_fp8_quantize", x, x.shape[-1], q, scales, n_rows, stream)
+
+
+def moe_fp8_quantize_silu(x, q, scales, n_rows=None, stream=None) -> None:
+    """moe_fp8_quantize of silu(x[:, :K]) * x[:, K:], x [M, 2K] (the output of a gate_up product)."""
+    fn = "moe_fp8_quantize_silu"
+    if x.shape[-1] % 2:
+        raise _bad(fn, f"x has {x.shape[-1]} columns: gate and up halves are equally wide")
+    _quantize(fn, x, x.shape[-1] // 2, q, scales, n_rows, stream)
+
+
+def moe_fp8_gemm(a, a_scales, w, w_scales, c, expert_offsets=None, sorted_pairs=None, k: int = 1,
+                 stream=None) -> None:
+    """c[i] = row (i, or sorted_pairs[i] // k) of a times the transposed weights of row i's expert.
+
+    a e4m3 [R, K] with scales fp32 [R, ceil(K/128)]; w e4m3 [E, N, K] (or [N, K]) contiguous with
+    scales fp32 [E, ceil(N/128), ceil(K/128)]; c [M, N] fp16, bf16 or fp32.  expert_offsets int32
+    [E+1] gives the groups of c's rows (None: one group); rows of c behind the last group are left
+    alone.  See the header for the rules."""
+    fn = "moe_fp8_gemm"
+    code, dev, ty = _row_dtype(fn, "c", c), c.device, _types()
+    M, N = c.shape
+    R, K = a.shape
+    E = w.shape[0] if w.dim() == 3 else 1
+    kb = -(-K // MOE_FP8_BLOCK)
+    _e4m3(fn, "a", a, dev)
+    _e4m3(fn, "w", w, dev)
+    if expert_offsets is not None and expert_offsets.numel() != E + 1:
+        raise _bad(fn, f"expert_offsets has {expert_offsets.numel()} entries for {E} experts")
+    _run_on(fn, dev, stream, a.data_ptr(), _rows(fn, "a", a, R, K, a.dtype, dev),
+            _flat(fn, "a_scales", a_scales, R * kb, ty["f32"], dev), R, _flat(fn, "w", w, E * N * K, w.dtype, dev),
+            _flat(fn, "w_scales", w_scales, E * -(-N // MOE_FP8_BLOCK) * kb, ty["f32"], dev), E, M, N, K,
+            None if expert_offsets is None else _flat(fn, "expert_offsets", expert_offsets, E + 1, ty["i32"], dev),
+            None if sorted_pairs is None else _flat(fn, "sorted_pairs", sorted_pairs, M, ty["i32"], dev), k,
+            c.data_ptr(), code, _rows(fn, "c", c, M, N, c.dtype, dev))
 
 
 # ---------------------------------------------------------------------------------------------

@@ -135,8 +135,6 @@ Workspace carve_workspace(void* base, int T, int E, int H, int I, int k, int I_s
   return w;
 }
 
-namespace {
-
 int check_route_args(int T, int E, int k) {
   if (T < 0 || E <= 0 || k <= 0) return set_error(MOE_EINVAL, "need T >= 0, E > 0, k > 0 (T=%d E=%d k=%d)", T, E, k);
   if (k > E) return set_error(MOE_EINVAL, "k=%d exceeds E=%d", k, E);
@@ -145,6 +143,8 @@ int check_route_args(int T, int E, int k) {
                      MOE_MAX_EXPERTS, MOE_MAX_TOPK, MOE_MAX_TOKENS, E, k, T);
   return MOE_OK;
 }
+
+namespace {
 
 int check_ffn_dims(int H, int I, int I_shared, bool has_shared) {
   if (H <= 0 || I <= 0 || H % kColChunk || I % kColChunk)

@@ -182,7 +182,8 @@ int layer_forward_ws(const float* logits, const uint16_t* x, int T, int E, int H
                      const moe_apq_block* table, const moe_apq_block* shared, int I_shared,
                      const float* shared_scale, int prefill_threshold, uint16_t* y, const Workspace& ws,
                      bool clear_err, int32_t* status, hipStream_t stream);
-// Argument checks shared by the layer entry points (host scalars only).
+// Argument checks shared by the entry points (host scalars only).
+int check_route_args(int T, int E, int k);
 int check_layer_args(const float* logits, const uint16_t* x, int T, int E, int H, int I, int k,
                      const moe_apq_block* table, const moe_apq_block* shared, int I_shared, uint16_t* y);
 int launch_apq_gemv(const moe_apq_block& blk, const uint16_t* x, int T, float* y,
@@ -222,6 +223,21 @@ int launch_substitute(const float* logits, int T, int E, int k, const uint8_t* r
                       hipStream_t stream);
 int launch_lynx_remap(const float* logits, int T, int E, int k, float bin_width, int32_t* ids,
                       int32_t* remapped, uint8_t* critical, hipStream_t stream);
+int launch_permute_tokens(const void* x, int dtype, int64_t x_stride, int T, int k, int E, int H,
+                          const int32_t* ids, const int32_t* offsets, const int32_t* pairs, void* xs,
+                          int64_t xs_stride, int32_t* rows, hipStream_t stream);
+// y[t] = sum_j gates[t,j] ys[rows[t,j]] + add[t]; gates (1) and add (0) may be null.
+int launch_combine_rows(const char* name, const void* ys, int dtype, int64_t ys_stride, int T, int k, int H,
+                        const int32_t* rows, const float* gates, const void* add, int64_t add_stride, void* y,
+                        int64_t y_stride, hipStream_t stream);
+int launch_combine_rows_grad(const void* dy, int dtype, int64_t dy_stride, const void* ys, int64_t ys_stride, int T,
+                             int k, int H, const int32_t* rows, const float* gates, void* dys, int64_t dys_stride,
+                             float* dgates, hipStream_t stream);
+int launch_fp8_quantize(const char* name, bool silu, const void* x, int dtype, int64_t x_stride, int M, int K,
+                        const int32_t* n_rows, uint8_t* q, int64_t q_stride, float* scales, hipStream_t stream);
+int launch_fp8_gemm(const uint8_t* a, int64_t lda, const float* a_scales, int a_rows, const uint8_t* w,
+                    const float* w_scales, int E, int M, int N, int K, const int32_t* offsets, const int32_t* pairs,
+                    int k, void* c, int dtype, int64_t ldc, hipStream_t stream);
 int launch_hbm_read_probe(const void* buf, size_t bytes, uint32_t* sink, hipStream_t stream);
 
 }  // namespace moeapq

@@ -43,6 +43,13 @@ __device__ __forceinline__ uint64_t readlane64(uint64_t v, int lane) {
   return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
+// v behind the wait states a DPP instruction needs after a change of EXEC: for a value that comes
+// out of divergent code and goes into a DPP reduction.
+__device__ __forceinline__ float dpp_settled(float v) {
+  asm volatile("s_nop 4" : "+v"(v));
+  return v;
+}
+
 template <int CTRL>
 __device__ __forceinline__ uint32_t max_dpp32(uint32_t v) {
   const uint32_t o = __builtin_amdgcn_update_dpp(0u, v, CTRL, 0xf, 0xf, false);

@@ -52,6 +52,13 @@ extern "C" {
 #define MOE_MAX_TOPK 32
 #define MOE_MAX_TOKENS 65536
 
+/* Element types of the row operators (moe_permute_tokens ... moe_fp8_gemm). */
+#define MOE_DTYPE_F16 0
+#define MOE_DTYPE_BF16 1
+#define MOE_DTYPE_F32 2
+#define MOE_MAX_ROW 1048576  /* columns of a row these operators take                          */
+#define MOE_FP8_BLOCK 128    /* columns (and weight rows) that share one scale                 */
+
 /* Substitution policies of moe_substitute ("Which Expert Misses Are Worth Waiting For?"). */
 #define MOE_POLICY_FETCH_ALL 0     /* fetch every miss (no substitution)                     */
 #define MOE_POLICY_GATE_RULE 1     /* fetch a miss if first choice or gate >= gate_threshold */
@@ -424,6 +431,97 @@ int moe_page_offload(moe_apq_block* table, int table_len, int index, const moe_a
 int moe_plan_widths(int n, const uint8_t* q_cur, const uint8_t* q_floor, const int32_t* rows,
                     const int32_t* cols, const float* damage, const float* mult,
                     int64_t target_bytes, uint8_t* q_new, int64_t* bytes_saved);
+
+/*
+ * Token rows sorted by expert and back, for expert products that take whole groups of rows
+ * (moe_fp8_gemm below, or a caller's own), with their gradients.
+ *
+ * Conventions of the row operators (these four, moe_fp8_quantize*, moe_fp8_gemm): `dtype` is a
+ * MOE_DTYPE_*; rows are contiguous, `*_stride` is the distance between rows in elements (>= the
+ * row's length); pointers need the alignment of one element and every row length is taken,
+ * unless stated.  H <= MOE_MAX_ROW.  Outputs may not overlap inputs.  Calls read nothing back and
+ * keep nothing, so any number of them may run at once on different streams.
+ *
+ * moe_permute_tokens: topk_ids [T][k], expert_offsets [E+1] and sorted_pairs [T*k] as given to and
+ *   written by moe_group_by_expert.
+ *     x_sorted[i] = x[sorted_pairs[i] / k] for i < P = expert_offsets[E]; rows from P on are left as
+ *     they were.
+ *     pair_rows (out int32 [T][k]): pair_rows[p] = i where sorted_pairs[i] = p, -1 for a pair whose
+ *     id is outside [0, E).
+ * moe_permute_tokens_backward: dx[t] = sum_j dx_sorted[pair_rows[t][j]] over the pairs with a row
+ *   (a token without any gets zeros).
+ * moe_unpermute_tokens: y[t] = sum_j g[t][j] y_sorted[pair_rows[t][j]] + add[t], over the pairs with a
+ *   row; gates fp32 [T][k] or NULL (= 1), add [T][H] or NULL (the shared expert's output, a
+ *   residual; its gradient is dy itself).
+ * moe_unpermute_tokens_backward: dy_sorted[pair_rows[t][j]] = g[t][j] dy[t];
+ *   dgates[t][j] = sum_h dy[t][h] y_sorted[pair_rows[t][j]][h] (fp32, 0 for a pair without a row).
+ *   Rows of dy_sorted that no pair names are left as they were.  Either output may be NULL;
+ *   y_sorted may be NULL when dgates is.
+ * Sums are fp32 in slot order (the dot product in a fixed order), rounded once; nothing depends on
+ * timing.  A pair_rows entry outside [0, T*k) counts as "no row".
+ * T = 0 is a no-op.  Errors: MOE_EINVAL (bad T/E/k/H, dtype, stride, NULL), MOE_EUNSUPPORTED
+ * (bounds), MOE_EHIP.
+ */
+int moe_permute_tokens(const void* x, int dtype, int64_t x_stride, int T, int k, int E, int H,
+                       const int32_t* topk_ids, const int32_t* expert_offsets, const int32_t* sorted_pairs,
+                       void* x_sorted, int64_t xs_stride, int32_t* pair_rows, void* stream);
+int moe_permute_tokens_backward(const void* dx_sorted, int dtype, int64_t dxs_stride, int T, int k, int H,
+                                const int32_t* pair_rows, void* dx, int64_t dx_stride, void* stream);
+int moe_unpermute_tokens(const void* y_sorted, int dtype, int64_t ys_stride, int T, int k, int H,
+                         const int32_t* pair_rows, const float* gates, const void* add, int64_t add_stride,
+                         void* y, int64_t y_stride, void* stream);
+int moe_unpermute_tokens_backward(const void* dy, int dtype, int64_t dy_stride, const void* y_sorted,
+                                  int64_t ys_stride, int T, int k, int H, const int32_t* pair_rows,
+                                  const float* gates, void* dy_sorted, int64_t dys_stride, float* dgates,
+                                  void* stream);
+
+/*
+ * Rows quantised to e4m3 (OCP, largest value 448) with one fp32 scale for each block of
+ * MOE_FP8_BLOCK columns (the last block of a row may be short).
+ *     v = x[r][c]                                              (moe_fp8_quantize,      x [M][K])
+ *     v = silu(x[r][c]) * x[r][K + c], silu(z) = z / (1 + e^-z) (moe_fp8_quantize_silu, x [M][2K])
+ *     m = max |v| over the block's finite values, at least 2^-100;  scale = m / 448
+ *     q = the e4m3 value nearest to v * (448 / m), ties to even
+ *   v is fp32 and is not rounded before it is quantised; both divisions are correctly rounded.  A
+ *   value that is not finite becomes e4m3's NaN (0x7f or 0xff) and leaves the rest of its block alone.
+ *   q out uint8 [M][q_stride], scales out fp32 [M][ceil(K/128)] contiguous.
+ *   n_rows: device int32 [1] or NULL: rows from *n_rows on are neither read nor written (e.g.
+ *   expert_offsets + E for sorted rows).
+ *   Bounds: 0 <= M <= MOE_MAX_TOKENS * MOE_MAX_TOPK (0: a no-op), 1 <= K <= MOE_MAX_ROW, M * K <= 2^39.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP.
+ */
+int moe_fp8_quantize(const void* x, int dtype, int64_t x_stride, int M, int K, const int32_t* n_rows,
+                     uint8_t* q, int64_t q_stride, float* scales, void* stream);
+int moe_fp8_quantize_silu(const void* x, int dtype, int64_t x_stride, int M, int K, const int32_t* n_rows,
+                          uint8_t* q, int64_t q_stride, float* scales, void* stream);
+
+/*
+ * Matrix product in e4m3 with a scale for each block of 128, grouped by expert or plain:
+ *     c[i][n] = sum_b a_scales[r][b] w_scales[e][n/128][b] sum_{j in block b} a[r][j] w[e][n][j]
+ *   for the rows i of expert e (expert_offsets[e] <= i < expert_offsets[e+1]); rows of c from
+ *   expert_offsets[E] on are left as they were.
+ *   a         e4m3 [a_rows][lda], lda % 16 == 0, 16-byte aligned; a_scales fp32 [a_rows][ceil(K/128)].
+ *   w         e4m3 [E][N][K] contiguous, 16-byte aligned; w_scales fp32 [E][ceil(N/128)][ceil(K/128)].
+ *   M         rows of c (T*k for sorted rows).
+ *   expert_offsets  device int32 [E+1] as moe_group_by_expert writes it, or NULL: one group of M
+ *             rows (E must be 1).  Values are taken into [0, M].
+ *   sorted_pairs    device int32 [M] or NULL.  Given: r = sorted_pairs[i] / k, taken into
+ *             [0, a_rows) (the rows of a are gathered while they are read, no sorted copy is made).
+ *             NULL: r = i, and a_rows >= M; k is ignored.
+ *   c         out dtype [M][ldc].
+ *   Bounds: E <= MOE_MAX_EXPERTS, 0 <= M <= MOE_MAX_TOKENS * MOE_MAX_TOPK (0: a no-op), 1 <= N <=
+ *   MOE_MAX_ROW, 16 <= K <= MOE_MAX_ROW with K % 16 == 0.
+ *   Accuracy: the sum over blocks is fp32, c is rounded once.  For fp32 c a block's products are
+ *   added in fp32; for 16-bit c the e4m3 matrix instruction adds them on a grid of 2^-13 of the
+ *   largest product in the block (a relative error of about 1.5e-5 on normal data).  e4m3 NaN in
+ *   a row of a or w reaches every element that row takes part in, and no other.
+ *   The gradient with respect to a is the same product with the weights and their scales
+ *   transposed ([E][K][N]: square blocks keep their scales).
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_EHIP.
+ */
+int moe_fp8_gemm(const uint8_t* a, int64_t lda, const float* a_scales, int a_rows, const uint8_t* w,
+                 const float* w_scales, int E, int M, int N, int K, const int32_t* expert_offsets,
+                 const int32_t* sorted_pairs, int k, void* c, int dtype, int64_t ldc, void* stream);
 
 /*
  * Diagnostic: read `bytes` of device memory at `buf` once, with the access pattern that streams

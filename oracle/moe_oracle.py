@@ -484,3 +484,127 @@ def rel_l2(a: np.ndarray, ref: np.ndarray) -> float:
     ref = np.asarray(ref, dtype=np.float64)
     den = np.linalg.norm(ref)
     return float(np.linalg.norm(a - ref) / den) if den > 0 else float(np.linalg.norm(a))
+
+
+# ------------------------------------------------------------------------------------------
+# Row operators: tokens sorted by expert and back, e4m3 quantising, the grouped e4m3 product
+# ------------------------------------------------------------------------------------------
+E4M3_BLOCK = 128
+E4M3_MAX = 448.0
+
+
+def pair_rows(sorted_pairs: np.ndarray, n_placed: int, pairs: int) -> np.ndarray:
+    """Sorted position of every pair, -1 for a pair that is not placed."""
+    rows = np.full(pairs, -1, dtype=np.int32)
+    for i in range(n_placed):
+        rows[sorted_pairs[i]] = i
+    return rows
+
+
+def unpermute_tokens(ys: np.ndarray, rows: np.ndarray, gates=None, add=None):
+    """(y, sum of the terms' magnitudes), both float64 [T, H]; rows [T, k], -1: no term."""
+    T, k = rows.shape
+    y = np.zeros((T, ys.shape[1]))
+    size = np.zeros_like(y)
+    for t in range(T):
+        for j in range(k):
+            if rows[t, j] < 0:
+                continue
+            term = ys[rows[t, j]].astype(np.float64) * (1.0 if gates is None else float(gates[t, j]))
+            y[t] += term
+            size[t] += np.abs(term)
+        if add is not None:
+            y[t] += add[t].astype(np.float64)
+            size[t] += np.abs(add[t].astype(np.float64))
+    return y, size
+
+
+def unpermute_tokens_grad(dy: np.ndarray, ys: np.ndarray, rows: np.ndarray, gates=None):
+    """(dys by placed row, dgates, sum of |dy * ys| per pair) in float64; rows [T, k]."""
+    T, k = rows.shape
+    dys = {}
+    dgates = np.zeros((T, k))
+    size = np.zeros((T, k))
+    for t in range(T):
+        d = dy[t].astype(np.float64)
+        for j in range(k):
+            if rows[t, j] < 0:
+                continue
+            dys[int(rows[t, j])] = d * (1.0 if gates is None else float(gates[t, j]))
+            prod = d * ys[rows[t, j]].astype(np.float64)
+            dgates[t, j] = prod.sum()
+            size[t, j] = np.abs(prod).sum()
+    return dys, dgates, size
+
+
+def e4m3_values() -> np.ndarray:
+    """The value of each of the 256 e4m3 codes: sign, 4 exponent bits (bias 7), 3 fraction bits;
+    exponent 0 is subnormal, the code with all of them set is NaN, there is no infinity."""
+    out = np.zeros(256)
+    for code in range(256):
+        exponent, fraction = (code >> 3) & 15, code & 7
+        v = fraction / 8 * 2.0 ** -6 if exponent == 0 else (1 + fraction / 8) * 2.0 ** (exponent - 7)
+        if exponent == 15 and fraction == 7:
+            v = np.nan
+        out[code] = -v if code & 128 else v
+    return out
+
+
+def e4m3_encode(v: np.ndarray) -> np.ndarray:
+    """Codes of the e4m3 values nearest to v (|v| < 464), ties to the even code; NaN for NaN."""
+    table = e4m3_values()[:127]            # magnitudes, ascending with the code
+    mag = np.abs(v)
+    hi = np.clip(np.searchsorted(table, np.nan_to_num(mag)), 0, 126)
+    lo = np.maximum(hi - 1, 0)
+    up, down = table[hi] - mag, mag - table[lo]
+    code = np.where((up < down) | ((up == down) & (hi % 2 == 0)), hi, lo)
+    code = np.where(np.isnan(mag), 127, code)
+    return (code + 128 * np.signbit(v)).astype(np.uint8)
+
+
+def fp8_quantize(v: np.ndarray):
+    """(codes uint8 [M, K], scales fp32 [M, ceil(K/128)]) of fp32 rows, with the two divisions and
+    the product rounded to fp32 as the definition has them."""
+    v = v.astype(np.float32)
+    M, K = v.shape
+    kb = -(-K // E4M3_BLOCK)
+    codes = np.zeros((M, K), dtype=np.uint8)
+    scales = np.zeros((M, kb), dtype=np.float32)
+    for b in range(kb):
+        cols = slice(b * E4M3_BLOCK, min(K, (b + 1) * E4M3_BLOCK))
+        block = v[:, cols]
+        fine = np.isfinite(block)
+        m = np.maximum(np.where(fine, np.abs(block), 0).max(axis=1), np.float32(2.0 ** -100)).astype(np.float32)
+        inv = (np.float32(E4M3_MAX) / m).astype(np.float32)
+        scaled = (np.where(fine, block, 0) * inv[:, None]).astype(np.float32)
+        codes[:, cols] = e4m3_encode(np.where(fine, scaled.astype(np.float64), np.nan))
+        scales[:, b] = m / np.float32(E4M3_MAX)
+    return codes, scales
+
+
+def fp8_dequantize(codes: np.ndarray, scales: np.ndarray, row_block: int = 1) -> np.ndarray:
+    """float64 values of codes [R, K] with scales [ceil(R/row_block), ceil(K/128)]."""
+    R, K = codes.shape
+    s = np.repeat(np.repeat(scales.astype(np.float64), row_block, axis=0)[:R], E4M3_BLOCK, axis=1)[:, :K]
+    return e4m3_values()[codes] * s
+
+
+def fp8_gemm(a, a_scales, w, w_scales, groups, source):
+    """(c, sum of the products' magnitudes, sum over blocks of the largest product a block can have)
+    in float64: rows i of groups[e] = range of rows, row i of c from row source[i] of a.
+    a [R, K], w [E, N, K] codes."""
+    n = max([g.stop for g in groups] + [0])
+    c = np.zeros((n, w.shape[1]))
+    size = np.zeros_like(c)
+    top = np.zeros_like(c)
+    for e, rows in enumerate(groups):
+        if len(rows) == 0:
+            continue
+        we = fp8_dequantize(w[e], w_scales[e], E4M3_BLOCK)
+        src = np.asarray(source)[list(rows)]
+        ae = fp8_dequantize(a[src], a_scales[src])
+        c[rows.start:rows.stop] = ae @ we.T
+        size[rows.start:rows.stop] = np.abs(ae) @ np.abs(we).T
+        for b in range(0, a.shape[1], E4M3_BLOCK):
+            top[rows.start:rows.stop] += np.outer(np.abs(ae[:, b:b + E4M3_BLOCK]).max(1), np.abs(we[:, b:b + E4M3_BLOCK]).max(1))
+    return c, size, top
