@@ -11,6 +11,7 @@
 // lane's four results are four neighbouring columns n of one row i of c and its scale sa is one
 // value.  The order of the 128 products inside a block does not matter, so lane (r, g) = (l % 16,
 // l / 16) simply takes the 16-byte pieces g and g + 4 of its row's block on both sides.
+#include <cstddef>
 #include <type_traits>
 
 #include "elements.hpp"
@@ -41,8 +42,8 @@ struct GemmArgs {
 };
 
 // ---- tiles of the groups ---------------------------------------------------------------------
-// The rows of group e are cut into tiles of BM rows; a tile of c is (row tile, column tile), and
-// all tiles are numbered group by group, inside a group column tile by column tile with the row
+// The n rows of a group are cut into ceil(n / BM) tiles of equal height (rounded up to 16 rows), so
+// that no tile is nearly empty; a tile of c is (row tile, column tile), and all tiles are numbered group by group, inside a group column tile by column tile with the row
 // tiles of one column tile side by side (they share its weights).
 struct Tile {
   int e, first, rows, col_tile;     // rows <= 0: no tile
@@ -53,6 +54,11 @@ __device__ __forceinline__ int group_rows(const GemmArgs& g, int e, int& first) 
   const int lo = g.offsets[min(e, g.E)], hi = g.offsets[min(e + 1, g.E)];
   first = min(max(lo, 0), g.M);
   return max(min(max(hi, 0), g.M) - first, 0);
+}
+
+template <int BM>
+__device__ __forceinline__ int tile_height(int n, int tiles) {
+  return tiles == 1 ? BM : (n + tiles * 16 - 1) / (tiles * 16) * 16;
 }
 
 // Workgroups go round the 8 dies in turn, so the tiles are dealt out in 8 contiguous runs, one to
@@ -77,9 +83,10 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& g, int col_tiles, uint
   uint32_t t = (block % 8) * per + block / 8;
   if (t >= tiles) return out;
   if (!g.offsets) {
+    const int high = tile_height<BM>(g.M, total);
     out.col_tile = t / total;
-    out.first = static_cast<int>(t % total) * BM;
-    out.rows = min(g.M - out.first, BM);
+    out.first = static_cast<int>(t % total) * high;
+    out.rows = min(g.M - out.first, high);
     return out;
   }
   for (int e0 = 0; e0 < g.E; e0 += 64) {
@@ -93,11 +100,11 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& g, int col_tiles, uint
       const int l = __builtin_ctzll(hit);
       const int mt_l = lane_int(mt, l);
       const uint32_t in = t - static_cast<uint32_t>(lane_int(upto, l) - mt_l) * col_tiles;
-      const int m = in % mt_l;
+      const int n_l = lane_int(n, l), from = static_cast<int>(in % mt_l) * tile_height<BM>(n_l, mt_l);
       out.e = e0 + l;
       out.col_tile = in / mt_l;
-      out.first = lane_int(first, l) + m * BM;
-      out.rows = min(lane_int(n, l) - m * BM, BM);
+      out.first = lane_int(first, l) + from;
+      out.rows = min(n_l - from, tile_height<BM>(n_l, mt_l));
       return out;
     }
     t -= all;
@@ -124,7 +131,7 @@ __device__ __forceinline__ f16x8 widen(int lo, int hi) {
   return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// One block's products of 16 weight rows and 16 rows of a.
+// One side of a block's products: 16 rows by 128, a lane's 32 bytes.
 //
 // The e4m3 instruction does not add its 128 products in fp32: it brings them to the exponent of the
 // largest and drops what lies below 2^-13 of it (a second product of 2^-13 of the first survives,
@@ -133,12 +140,26 @@ __device__ __forceinline__ f16x8 widen(int lo, int hi) {
 // results (FINE) both sides are widened to fp16, which holds every e4m3 value, and the fp16
 // instruction adds in fp32: 3e-8, at half the matrix rate.
 template <bool FINE>
-__device__ __forceinline__ f32x4 mfma_block(const i32x8& w, const i32x8& a) {
-  if (!FINE) return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+struct Side {
+  i32x8 v;
+  __device__ __forceinline__ explicit Side(const i32x8& x) : v(x) {}
+};
+template <>
+struct Side<true> {
+  f16x8 v[4];
+  __device__ __forceinline__ explicit Side(const i32x8& x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = widen(x[2 * i], x[2 * i + 1]);
+  }
+};
+
+__device__ __forceinline__ f32x4 mfma_block(const Side<false>& w, const Side<false>& a) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, a.v, f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma_block(const Side<true>& w, const Side<true>& a) {
   f32x4 p{0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    p = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen(w[2 * i], w[2 * i + 1]), widen(a[2 * i], a[2 * i + 1]), p, 0, 0, 0);
+  for (int i = 0; i < 4; ++i) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.v[i], a.v[i], p, 0, 0, 0);
   return p;
 }
 
@@ -168,6 +189,7 @@ constexpr int kStreamWaves = kStreamThreads / 64;
 template <int MT, int NT, int DT>
 __global__ __launch_bounds__(kStreamThreads) void fp8_gemm_stream_kernel(GemmArgs g, int col_tiles) {
   constexpr int BM = MT * 16, BN = NT * 16;
+  constexpr bool kFine = DT == MOE_DTYPE_F32;
   __shared__ float part[kStreamWaves - 1][BN][BM + 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, piece = lane >> 4;
@@ -203,9 +225,10 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_gemm_stream_kernel(GemmArg
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       s[i] *= sw;
+      const Side<kFine> as(a[i]);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const f32x4 p = mfma_block<DT == MOE_DTYPE_F32>(w[j], a[i]);
+        const f32x4 p = mfma_block(Side<kFine>(w[j]), as);
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[j][i][v] = fmaf(p[v], s[i], acc[j][i][v]);
       }
@@ -243,22 +266,276 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_gemm_stream_kernel(GemmArg
   }
 }
 
-template <int MT, int NT>
-int launch_stream(const GemmArgs& g, int dtype, hipStream_t stream) {
-  constexpr int BM = MT * 16, BN = NT * 16;
-  const int col_tiles = (g.N + BN - 1) / BN;
-  // at most one partly filled row tile per group with rows
+// ---- many rows ---------------------------------------------------------------------------------
+// A workgroup of four wavefronts holds a tile of up to 128 rows by 256 columns, each wavefront all
+// rows by 64 columns.  Every block of a is used by all four, so it goes through LDS (three stages,
+// filled by direct loads two blocks ahead); every block of weights is used by one wavefront only, so
+// it goes straight into that one's registers, one block ahead.  That leaves LDS with half the matrix
+// instructions' time.  The scale products sa * sw of the next block are laid out in LDS beside it.
+constexpr int kTileThreads = 256;
+constexpr int kTileN = 256, kWaveN = 4;      // kWaveN: 16-column pieces of a wavefront
+constexpr int kStages = 3;
+// Rows of the highest tile: its accumulators (4 registers for each 16 rows and 16 columns) fill half
+// the registers two wavefronts per SIMD leave; widening to fp16 needs 64 more for the weights.
+template <int DT>
+constexpr int kTileM = DT == MOE_DTYPE_F32 ? 64 : 128;
+
+#define MOE_LDS __attribute__((address_space(3)))
+
+// 16 bytes per lane from rsrc + offset + uniform into LDS at lds_addr + 16 * lane.  The buffer form:
+// the compiler takes the global one for a flat access and waits for every load in flight.
+__device__ __forceinline__ void lds_load16(uint32_t lds_addr, __amdgpu_buffer_rsrc_t rsrc, uint32_t offset,
+                                           uint32_t uniform) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (MOE_LDS void*)static_cast<uintptr_t>(lds_addr), 16, offset, uniform,
+                                           0, 0);
+}
+
+template <int BM>
+struct TileLds {
+  uint8_t a[kStages][BM * kBlock];
+  float scale[2][2][BM];            // [block parity][128-column half][row]
+};
+
+// A lane value the compiler recomputes addresses from instead of keeping them (they are 64 bits wide
+// and this kernel has no register to spare).
+__device__ __forceinline__ uint32_t opaque(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+template <int TM, int DT>
+__device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, TileLds<kTileM<DT>>& lds) {
+  constexpr int BM = kTileM<DT>, kStageBytes = BM * kBlock;
+  constexpr bool kFine = DT == MOE_DTYPE_F32;
+  using Op = Side<kFine>;
+  constexpr int kDma = TM / 2;      // direct loads of one stage per wavefront (1 KiB = 8 rows each)
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, piece = lane >> 4;
+  const int nt0 = tile.col_tile * kTileN, n0 = nt0 + wave * 16 * kWaveN;
+  const uint8_t* w_base = g.w + (static_cast<int64_t>(tile.e) * g.N + nt0) * g.K;
+  uint32_t w_off[kWaveN];
+#pragma unroll
+  for (int j = 0; j < kWaveN; ++j)
+    w_off[j] = static_cast<uint32_t>(min(n0 + j * 16 + r, g.N - 1) - nt0) * g.K + piece * 16;
+  // Row `8 q + lane / 8` of the stage; its 16-byte piece c sits at slot c ^ (row % 8), so that the 16
+  // rows of a fragment read their pieces from all banks.  Offsets of 32 bits: from the tile's
+  // first row, or from the start of a if its rows are gathered (the entry point keeps those below 4 GiB).
+  const int chunk = (lane & 7) ^ (lane >> 3);
+  const int64_t a_base = g.pairs ? 0 : source_row(g, tile.first);
+  const auto a_rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.a + a_base * g.lda), 0, -1, 0x00027000);
+  uint32_t a_off[kDma];
+#pragma unroll
+  for (int q = 0; q < kDma; ++q) {
+    const int m = min((wave * kDma + q) * 8 + (lane >> 3), tile.rows - 1);
+    a_off[q] = static_cast<uint32_t>((source_row(g, tile.first + m) - a_base) * g.lda) + chunk * 16;
+  }
+  const int s_row = threadIdx.x & 127;
+  const uint32_t s_src = static_cast<uint32_t>(source_row(g, tile.first + min(s_row, tile.rows - 1)));
+  const float* sw = g.w_scales + (static_cast<int64_t>(tile.e) * g.nb + min(nt0 / kBlock + (wave >> 1), g.nb - 1)) * g.kb;
+  const uint32_t lds_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS uint8_t*)&lds.a[0][0]));
+  const uint32_t scale_at = lds_at + static_cast<uint32_t>(offsetof(TileLds<BM>, scale)) + ((wave >> 1) * BM + s_row) * 4;
+
+  auto load_w = [&](int kb, int j) {
+    union {
+      u32x4 half[2];
+      i32x8 all;
+    } u;
+    const uint8_t* p = w_base + static_cast<int64_t>(kb) * kBlock + opaque(w_off[j]);
+    u.half[0] = *reinterpret_cast<const u32x4*>(p);
+    u.half[1] = *reinterpret_cast<const u32x4*>(p + 64);
+    return u.all;
+  };
+  auto stage_a = [&](int kb, int stage, int q) {
+    lds_load16(lds_at + stage * kStageBytes + (wave * kDma + q) * 1024, a_rsrc, a_off[q], kb * kBlock);
+  };
+  auto load_scale = [&](int kb) { return g.a_scales[static_cast<uint64_t>(opaque(s_src)) * g.kb + kb]; };
+  // In assembly, since the compiler would hold a plain LDS store until every direct load has landed.
+  auto store_scale = [&](int kb, float s) {
+    if (s_row < BM)
+      asm volatile("ds_write_b32 %0, %1" : : "v"(scale_at + (kb & 1) * (2 * BM * 4)), "v"(s) : "memory");
+  };
+
+  f32x4 acc[TM][kWaveN] = {};
+  const int a_at = r * kBlock + ((piece ^ (r & 7)) << 4);
+  // One block.  The next piece of a is read one row step ahead and results are added two matrix
+  // instructions after theirs, so that neither is waited for; `ahead(n)` issues the loads of the
+  // blocks to come between them.
+  auto multiply = [&](int kb, int stage, const Op (&w)[kWaveN], auto&& ahead) {
+    const uint8_t* a0 = &lds.a[stage][a_at];
+    const uint8_t* a1 = &lds.a[stage][a_at ^ 64];
+    const float* f = &lds.scale[kb & 1][wave >> 1][r];
+    auto read_a = [&](int i) {
+      union {
+        u32x4 half[2];
+        i32x8 all;
+      } u;
+      u.half[0] = *reinterpret_cast<const u32x4*>(a0 + i * 16 * kBlock);
+      u.half[1] = *reinterpret_cast<const u32x4*>(a1 + i * 16 * kBlock);
+      return u.all;
+    };
+    constexpr int kSteps = TM * kWaveN, kLag = 2;
+    i32x8 a[2];
+    float s[3];
+    f32x4 p[kLag + 1];
+    a[0] = read_a(0);
+    s[0] = f[0];
+    Op op(a[0]);
+    auto add = [&](int n) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        acc[n / kWaveN][n % kWaveN][v] = fmaf(p[n % (kLag + 1)][v], s[n / kWaveN % 3], acc[n / kWaveN][n % kWaveN][v]);
+    };
+#pragma unroll
+    for (int n = 0; n < kSteps; ++n) {
+      const int i = n / kWaveN, j = n % kWaveN;
+      if (j == 0) {
+        op = Op(a[i & 1]);
+        if (i + 1 < TM) {
+          a[(i + 1) & 1] = read_a(i + 1);
+          s[(i + 1) % 3] = f[(i + 1) * 16];
+        }
+      }
+      p[n % (kLag + 1)] = mfma_block(w[j], op);
+      __builtin_amdgcn_sched_barrier(0);
+      ahead(n);
+      if (n >= kLag) add(n - kLag);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int n = kSteps - kLag; n < kSteps; ++n) add(n);
+  };
+
+  i32x8 w0[kWaveN], w1[kWaveN];
+  const int full = g.K / kBlock, last = full - 1;
+  if (full > 0) {
+#pragma unroll
+    for (int q = 0; q < kDma; ++q) stage_a(0, 0, q);
+#pragma unroll
+    for (int j = 0; j < kWaveN; ++j) w0[j] = load_w(0, j);
+    store_scale(0, load_scale(0) * sw[0]);
+#pragma unroll
+    for (int q = 0; q < kDma; ++q) stage_a(min(1, last), 1, q);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kDma) : "memory");
+    __builtin_amdgcn_s_barrier();
+    int stage = 0;
+    // The next block's weights and scales and the one after's rows of a are on their way while this
+    // one is multiplied.
+    auto step = [&](int kb, i32x8 (&now)[kWaveN], i32x8 (&next)[kWaveN]) {
+      const int kn = min(kb + 1, last), stage_to = stage == 0 ? 2 : stage - 1;
+      const Op w[kWaveN] = {Op(now[0]), Op(now[1]), Op(now[2]), Op(now[3])};
+      if (kFine) __builtin_amdgcn_sched_barrier(0);
+      const float s_a = load_scale(kn), s_w = sw[kn];
+      multiply(kb, stage, w, [&](int n) {
+        if (n < kWaveN) next[n] = load_w(kn, n);
+        else if (n < kWaveN + kDma) stage_a(min(kb + 2, last), stage_to, n - kWaveN);
+      });
+      store_scale(kb + 1, s_a * s_w);
+      // everything but the rows of a issued last has landed
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kDma) : "memory");
+      __builtin_amdgcn_s_barrier();
+      stage = stage == 2 ? 0 : stage + 1;
+    };
+    int kb = 0;
+    if constexpr (kFine) {   // the widened weights are a copy: the next block's go where theirs came from
+      for (; kb <= last; ++kb) step(kb, w0, w0);
+    } else {
+      for (; kb < last; kb += 2) {
+        step(kb, w0, w1);
+        step(kb + 1, w1, w0);
+      }
+      if (kb == last) step(kb, w0, w1);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");   // the last stages' loads
+    __builtin_amdgcn_s_barrier();
+  }
+  // A short last block, not overlapped: the weights behind the row's end are zero, a's pieces there
+  // are read from the row's start (a row that holds NaN gives NaN anyway).
+  if (full < g.kb) {
+    store_scale(full, load_scale(full) * sw[full]);
+#pragma unroll
+    for (int q = 0; q < kDma; ++q) {
+      const uint32_t at = full * kBlock + chunk * 16 < g.K ? full * kBlock : -(chunk * 16);
+      lds_load16(lds_at + (wave * kDma + q) * 1024, a_rsrc, a_off[q] + at, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kWaveN; ++j) w0[j] = load_pieces<true>(w_base + w_off[j] - piece * 16, full, g.K, piece);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+    __builtin_amdgcn_s_barrier();
+    const Op w[kWaveN] = {Op(w0[0]), Op(w0[1]), Op(w0[2]), Op(w0[3])};
+    multiply(full, 0, w, [](int) {});
+  }
+
+  using T = typename Elem<DT>::T;
+  T* c = static_cast<T*>(g.c);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = i * 16 + r;
+    if (m < tile.rows) {
+      T* row = c + static_cast<int64_t>(tile.first + m) * g.ldc;
+#pragma unroll
+      for (int j = 0; j < kWaveN; ++j) {
+        const int n = n0 + j * 16 + piece * 4;
+        struct __attribute__((packed, aligned(kElemSize<DT>))) Four { T e[4]; };
+        if (n + 4 <= g.N) {
+          *reinterpret_cast<Four*>(row + n) = Four{{static_cast<T>(acc[i][j][0]), static_cast<T>(acc[i][j][1]),
+                                                    static_cast<T>(acc[i][j][2]), static_cast<T>(acc[i][j][3])}};
+        } else {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (n + v < g.N) row[n + v] = static_cast<T>(acc[i][j][v]);
+        }
+      }
+    }
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kTileThreads, 2) void fp8_gemm_tile_kernel(GemmArgs g, int col_tiles) {
+  __shared__ __align__(1024) TileLds<kTileM<DT>> lds;
+  const Tile tile = find_tile<kTileM<DT>>(g, col_tiles, blockIdx.x);
+  if (tile.rows <= 0) return;
+  if (kTileM<DT> > 96 && tile.rows > 96) gemm_tile<kTileM<DT> / 16, DT>(g, tile, lds);
+  else if (kTileM<DT> > 64 && tile.rows > 64) gemm_tile<kTileM<DT> * 3 / 64, DT>(g, tile, lds);
+  else if (tile.rows > 32) gemm_tile<4, DT>(g, tile, lds);
+  else gemm_tile<2, DT>(g, tile, lds);
+}
+
+// Workgroups for tiles of BM by BN: every group with rows may have one partly filled row tile.
+int tile_blocks(const GemmArgs& g, int BM, int BN, uint32_t* blocks, int* col_tiles) {
+  *col_tiles = (g.N + BN - 1) / BN;
   const int64_t row_tiles = (static_cast<int64_t>(g.M) + BM - 1) / BM + (g.offsets ? min(g.E, g.M) : 0);
-  const uint64_t blocks = (static_cast<uint64_t>(row_tiles) * col_tiles + 7) / 8 * 8;
-  if (blocks >> 31) return set_error(MOE_EUNSUPPORTED, "moe_fp8_gemm: %llu tiles are more than one launch takes",
-                                     static_cast<unsigned long long>(blocks));
+  const int64_t n = (row_tiles * *col_tiles + 7) / 8 * 8;
+  if (n >> 31)
+    return set_error(MOE_EUNSUPPORTED, "moe_fp8_gemm: %lld tiles are more than one launch takes", static_cast<long long>(n));
+  *blocks = static_cast<uint32_t>(n);
+  return MOE_OK;
+}
+
+template <int DT>
+int launch_tile(const GemmArgs& g, hipStream_t stream) {
+  uint32_t blocks;
+  int col_tiles;
+  if (int rc = tile_blocks(g, kTileM<DT>, kTileN, &blocks, &col_tiles)) return rc;
   ProfileScope prof("fp8_gemm", stream);
-  with_dtype(dtype, [&](auto dt) {
-    constexpr int DT = decltype(dt)::value;
-    hipLaunchKernelGGL((fp8_gemm_stream_kernel<MT, NT, DT>), dim3(static_cast<uint32_t>(blocks)), dim3(kStreamThreads),
-                       0, stream, g, col_tiles);
-  });
+  hipLaunchKernelGGL(fp8_gemm_tile_kernel<DT>, dim3(blocks), dim3(kTileThreads), 0, stream, g, col_tiles);
   return check_launch("fp8_gemm");
+}
+
+template <int MT, int NT, int DT>
+int launch_stream(const GemmArgs& g, hipStream_t stream) {
+  uint32_t blocks;
+  int col_tiles;
+  if (int rc = tile_blocks(g, MT * 16, NT * 16, &blocks, &col_tiles)) return rc;
+  ProfileScope prof("fp8_gemm", stream);
+  hipLaunchKernelGGL((fp8_gemm_stream_kernel<MT, NT, DT>), dim3(blocks), dim3(kStreamThreads), 0, stream, g, col_tiles);
+  return check_launch("fp8_gemm");
+}
+
+template <int DT>
+int launch_gemm(const GemmArgs& g, hipStream_t stream) {
+  if (g.M <= 16 * g.E) return launch_stream<1, 2, DT>(g, stream);
+  if (g.M <= 64 * g.E) return launch_stream<2, 2, DT>(g, stream);
+  return launch_tile<DT>(g, stream);
 }
 
 }  // namespace
@@ -268,8 +545,9 @@ int launch_fp8_gemm(const uint8_t* a, int64_t lda, const float* a_scales, int a_
                     int k, void* c, int dtype, int64_t ldc, hipStream_t stream) {
   const GemmArgs g{a, lda, a_scales, a_rows, w, w_scales, E, M, N, K, (K + kBlock - 1) / kBlock,
                    (N + kBlock - 1) / kBlock, offsets, pairs, k, c, ldc};
-  if (M <= 16 * E) return launch_stream<1, 2>(g, dtype, stream);
-  return launch_stream<2, 2>(g, dtype, stream);
+  int rc = MOE_OK;
+  with_dtype(dtype, [&](auto dt) { rc = launch_gemm<decltype(dt)::value>(g, stream); });
+  return rc;
 }
 
 }  // namespace moeapq

@@ -159,7 +159,8 @@ int moe_fp8_gemm(const uint8_t* a, int64_t lda, const float* a_scales, int a_row
   if (int rc = check_row("K", K)) return rc;
   if (K % 16) return set_error(MOE_EUNSUPPORTED, "need K %% 16 == 0 (K=%d)", K);
   if (int rc = check_stride("a", lda, K)) return rc;
-  if (lda % 16) return set_error(MOE_EUNSUPPORTED, "need lda %% 16 == 0 (lda=%lld)", static_cast<long long>(lda));
+  if (lda % 16 || lda > (1 << 24))
+    return set_error(MOE_EUNSUPPORTED, "need lda %% 16 == 0 and lda <= 2^24 (lda=%lld)", static_cast<long long>(lda));
   if (int rc = check_stride("c", ldc, N)) return rc;
   if (!expert_offsets && E != 1) return set_error(MOE_EINVAL, "E=%d groups need expert_offsets", E);
   if (M == 0) return MOE_OK;
@@ -168,6 +169,9 @@ int moe_fp8_gemm(const uint8_t* a, int64_t lda, const float* a_scales, int a_row
     return set_error(MOE_EINVAL, "a has %d rows for M=%d", a_rows, M);
   if (sorted_pairs && (k <= 0 || k > MOE_MAX_TOPK))
     return set_error(MOE_EINVAL, "k=%d outside 1..%d", k, MOE_MAX_TOPK);
+  if (sorted_pairs && a_rows * lda >= (int64_t{1} << 32))
+    return set_error(MOE_EUNSUPPORTED, "gathered rows of a must lie within 4 GiB (%d rows of stride %lld)", a_rows,
+                     static_cast<long long>(lda));
   if ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(w)) & 15)
     return set_error(MOE_EINVAL, "a and w must be 16-byte aligned");
   if (int rc = check_align("c", c, dtype)) return rc;

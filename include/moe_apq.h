@@ -500,14 +500,14 @@ int moe_fp8_quantize_silu(const void* x, int dtype, int64_t x_stride, int M, int
  *     c[i][n] = sum_b a_scales[r][b] w_scales[e][n/128][b] sum_{j in block b} a[r][j] w[e][n][j]
  *   for the rows i of expert e (expert_offsets[e] <= i < expert_offsets[e+1]); rows of c from
  *   expert_offsets[E] on are left as they were.
- *   a         e4m3 [a_rows][lda], lda % 16 == 0, 16-byte aligned; a_scales fp32 [a_rows][ceil(K/128)].
+ *   a         e4m3 [a_rows][lda], lda % 16 == 0 and at most 2^24, 16-byte aligned; a_scales fp32 [a_rows][ceil(K/128)].
  *   w         e4m3 [E][N][K] contiguous, 16-byte aligned; w_scales fp32 [E][ceil(N/128)][ceil(K/128)].
  *   M         rows of c (T*k for sorted rows).
  *   expert_offsets  device int32 [E+1] as moe_group_by_expert writes it, or NULL: one group of M
  *             rows (E must be 1).  Values are taken into [0, M].
  *   sorted_pairs    device int32 [M] or NULL.  Given: r = sorted_pairs[i] / k, taken into
- *             [0, a_rows) (the rows of a are gathered while they are read, no sorted copy is made).
- *             NULL: r = i, and a_rows >= M; k is ignored.
+ *             [0, a_rows) (the rows of a are gathered while they are read, no sorted copy is made;
+ *             a_rows * lda must stay below 4 GiB then).  NULL: r = i, and a_rows >= M; k is ignored.
  *   c         out dtype [M][ldc].
  *   Bounds: E <= MOE_MAX_EXPERTS, 0 <= M <= MOE_MAX_TOKENS * MOE_MAX_TOPK (0: a no-op), 1 <= N <=
  *   MOE_MAX_ROW, 16 <= K <= MOE_MAX_ROW with K % 16 == 0.

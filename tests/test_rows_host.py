@@ -90,7 +90,7 @@ def test_quantize_silu_needs_both_halves_in_the_row():
 @pytest.mark.parametrize("change,code", [
     (dict(E=0), BAD), (dict(E=1025), UNSUP), (dict(M=-1), BAD), (dict(M=(1 << 21) + 1), UNSUP), (dict(N=0), BAD),
     (dict(K=0), BAD), (dict(K=24), UNSUP), (dict(K=(1 << 20) + 16, lda=1 << 21), UNSUP), (dict(lda=240), BAD),
-    (dict(lda=264), UNSUP), (dict(ldc=63), BAD), (dict(dtype=3), BAD), (dict(offsets=None), BAD), (dict(a=None), BAD),
+    (dict(lda=264), UNSUP), (dict(lda=(1 << 24) + 16), UNSUP), (dict(pairs=FAKE, a_rows=1 << 16, lda=1 << 16), UNSUP), (dict(ldc=63), BAD), (dict(dtype=3), BAD), (dict(offsets=None), BAD), (dict(a=None), BAD),
     (dict(a_scales=None), BAD), (dict(w=None), BAD), (dict(w_scales=None), BAD), (dict(c=None), BAD),
     (dict(a_rows=7), BAD), (dict(a_rows=0, pairs=FAKE), BAD), (dict(pairs=FAKE, k=0), BAD), (dict(pairs=FAKE, k=33), BAD),
     (dict(a=FAKE + 8), BAD), (dict(w=FAKE + 4), BAD), (dict(c=FAKE + 1), BAD), (dict(M=0), OK),
