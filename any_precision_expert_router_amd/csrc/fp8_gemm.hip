@@ -271,7 +271,7 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_gemm_stream_kernel(GemmArg
 // rows by 64 columns.  Every block of a is used by all four, so it goes through LDS (three stages,
 // filled by direct loads two blocks ahead); every block of weights is used by one wavefront only, so
 // it goes straight into that one's registers, one block ahead.  That leaves LDS with half the matrix
-// instructions' time.  The scale products sa * sw of the next block are laid out in LDS beside it.
+// instructions' time.  The scales lie in LDS beside it.
 constexpr int kTileThreads = 256;
 constexpr int kTileN = 256, kWaveN = 4;      // kWaveN: 16-column pieces of a wavefront
 constexpr int kStages = 3;
@@ -290,10 +290,15 @@ __device__ __forceinline__ void lds_load16(uint32_t lds_addr, __amdgpu_buffer_rs
                                            0, 0);
 }
 
+// The scales of a and of the weights for kScaleBlocks blocks at a time, a row's fetched together: one
+// value per row and block would take as many L2 requests as half the weights do.
+constexpr int kScaleBlocks = 32;
+
 template <int BM>
 struct TileLds {
   uint8_t a[kStages][BM * kBlock];
-  float scale[2][2][BM];            // [block parity][128-column half][row]
+  float a_scale[kScaleBlocks][BM];
+  float w_scale[2][kScaleBlocks];   // of the tile's two 128-column halves
 };
 
 // A lane value the compiler recomputes addresses from instead of keeping them (they are 64 bits wide
@@ -329,11 +334,34 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
     const int m = min((wave * kDma + q) * 8 + (lane >> 3), tile.rows - 1);
     a_off[q] = static_cast<uint32_t>((source_row(g, tile.first + m) - a_base) * g.lda) + chunk * 16;
   }
-  const int s_row = threadIdx.x & 127;
-  const uint32_t s_src = static_cast<uint32_t>(source_row(g, tile.first + min(s_row, tile.rows - 1)));
-  const float* sw = g.w_scales + (static_cast<int64_t>(tile.e) * g.nb + min(nt0 / kBlock + (wave >> 1), g.nb - 1)) * g.kb;
   const uint32_t lds_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS uint8_t*)&lds.a[0][0]));
-  const uint32_t scale_at = lds_at + static_cast<uint32_t>(offsetof(TileLds<BM>, scale)) + ((wave >> 1) * BM + s_row) * 4;
+  // Scales of blocks [kb, kb + kScaleBlocks) into LDS; the caller waits and synchronises.  In
+  // assembly, since the compiler would hold plain LDS stores until every direct load has landed.
+  auto store_scales = [&](int kb) {
+    constexpr int kParts = kTileThreads / BM, kEach = kScaleBlocks / kParts;
+    const int tid = opaque(threadIdx.x);   // nothing of this is kept in registers between chunks
+    const int row = tid / kParts, b0 = tid % kParts * kEach;
+    const float* sa = g.a_scales + source_row(g, tile.first + min(row, tile.rows - 1)) * g.kb + kb;
+    const int n = g.kb - kb;
+    const uint32_t to = lds_at + static_cast<uint32_t>(offsetof(TileLds<BM>, a_scale)) + (b0 * BM + row) * 4;
+    constexpr int kGroup = 8;   // in flight at once: the accumulators leave no registers for more
+#pragma unroll
+    for (int i0 = 0; i0 < kEach; i0 += kGroup) {
+      float v[kGroup];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) v[i] = sa[min(b0 + i0 + i, n - 1)];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i)
+        asm volatile("ds_write_b32 %0, %1 offset:%2" : : "v"(to), "v"(v[i]), "n"((i0 + i) * BM * 4) : "memory");
+    }
+    if (tid < 2 * kScaleBlocks) {
+      const int half = tid / kScaleBlocks, i = tid % kScaleBlocks;
+      const float w = g.w_scales[(static_cast<int64_t>(tile.e) * g.nb + min(nt0 / kBlock + half, g.nb - 1)) * g.kb + kb +
+                                 min(i, n - 1)];
+      asm volatile("ds_write_b32 %0, %1"
+                   : : "v"(lds_at + static_cast<uint32_t>(offsetof(TileLds<BM>, w_scale)) + tid * 4), "v"(w) : "memory");
+    }
+  };
 
   auto load_w = [&](int kb, int j) {
     union {
@@ -348,13 +376,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
   auto stage_a = [&](int kb, int stage, int q) {
     lds_load16(lds_at + stage * kStageBytes + (wave * kDma + q) * 1024, a_rsrc, a_off[q], kb * kBlock);
   };
-  auto load_scale = [&](int kb) { return g.a_scales[static_cast<uint64_t>(opaque(s_src)) * g.kb + kb]; };
-  // In assembly, since the compiler would hold a plain LDS store until every direct load has landed.
-  auto store_scale = [&](int kb, float s) {
-    if (s_row < BM)
-      asm volatile("ds_write_b32 %0, %1" : : "v"(scale_at + (kb & 1) * (2 * BM * 4)), "v"(s) : "memory");
-  };
-
   f32x4 acc[TM][kWaveN] = {};
   const int a_at = r * kBlock + ((piece ^ (r & 7)) << 4);
   // One block.  The next piece of a is read one row step ahead and results are added two matrix
@@ -363,7 +384,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
   auto multiply = [&](int kb, int stage, const Op (&w)[kWaveN], auto&& ahead) {
     const uint8_t* a0 = &lds.a[stage][a_at];
     const uint8_t* a1 = &lds.a[stage][a_at ^ 64];
-    const float* f = &lds.scale[kb & 1][wave >> 1][r];
+    const float* f = &lds.a_scale[kb % kScaleBlocks][r];
+    const float sw = lds.w_scale[wave >> 1][kb % kScaleBlocks];
     auto read_a = [&](int i) {
       union {
         u32x4 half[2];
@@ -378,7 +400,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
     float s[3];
     f32x4 p[kLag + 1];
     a[0] = read_a(0);
-    s[0] = f[0];
+    s[0] = f[0] * sw;
     Op op(a[0]);
     auto add = [&](int n) {
 #pragma unroll
@@ -392,7 +414,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
         op = Op(a[i & 1]);
         if (i + 1 < TM) {
           a[(i + 1) & 1] = read_a(i + 1);
-          s[(i + 1) % 3] = f[(i + 1) * 16];
+          s[(i + 1) % 3] = f[(i + 1) * 16] * sw;
         }
       }
       p[n % (kLag + 1)] = mfma_block(w[j], op);
@@ -412,24 +434,24 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
     for (int q = 0; q < kDma; ++q) stage_a(0, 0, q);
 #pragma unroll
     for (int j = 0; j < kWaveN; ++j) w0[j] = load_w(0, j);
-    store_scale(0, load_scale(0) * sw[0]);
 #pragma unroll
     for (int q = 0; q < kDma; ++q) stage_a(min(1, last), 1, q);
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kDma) : "memory");
-    __builtin_amdgcn_s_barrier();
     int stage = 0;
     // The next block's weights and scales and the one after's rows of a are on their way while this
     // one is multiplied.
     auto step = [&](int kb, i32x8 (&now)[kWaveN], i32x8 (&next)[kWaveN]) {
+      if (kb % kScaleBlocks == 0) {
+        store_scales(kb);
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kDma) : "memory");
+        __builtin_amdgcn_s_barrier();
+      }
       const int kn = min(kb + 1, last), stage_to = stage == 0 ? 2 : stage - 1;
       const Op w[kWaveN] = {Op(now[0]), Op(now[1]), Op(now[2]), Op(now[3])};
       if (kFine) __builtin_amdgcn_sched_barrier(0);
-      const float s_a = load_scale(kn), s_w = sw[kn];
       multiply(kb, stage, w, [&](int n) {
         if (n < kWaveN) next[n] = load_w(kn, n);
         else if (n < kWaveN + kDma) stage_a(min(kb + 2, last), stage_to, n - kWaveN);
       });
-      store_scale(kb + 1, s_a * s_w);
       // everything but the rows of a issued last has landed
       asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kDma) : "memory");
       __builtin_amdgcn_s_barrier();
@@ -451,7 +473,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
   // A short last block, not overlapped: the weights behind the row's end are zero, a's pieces there
   // are read from the row's start (a row that holds NaN gives NaN anyway).
   if (full < g.kb) {
-    store_scale(full, load_scale(full) * sw[full]);
+    if (full % kScaleBlocks == 0) store_scales(full);
 #pragma unroll
     for (int q = 0; q < kDma; ++q) {
       const uint32_t at = full * kBlock + chunk * 16 < g.K ? full * kBlock : -(chunk * 16);
