@@ -42,7 +42,7 @@ struct GemmArgs {
 };
 
 // ---- tiles of the groups ---------------------------------------------------------------------
-// The n rows of a group are cut into ceil(n / BM) tiles of equal height (rounded up to 16 rows), so
+// The n rows of a group are cut into ceil(n / bm) tiles of equal height (rounded up to 16 rows), so
 // that no tile is nearly empty; a tile of c is (row tile, column tile), and all tiles are numbered group by group, inside a group column tile by column tile with the row
 // tiles of one column tile side by side (they share its weights).
 struct Tile {
@@ -56,15 +56,11 @@ __device__ __forceinline__ int group_rows(const GemmArgs& g, int e, int& first) 
   return max(min(max(hi, 0), g.M) - first, 0);
 }
 
-template <int BM>
-__device__ __forceinline__ int tile_height(int n, int tiles) {
-  return tiles == 1 ? BM : (n + tiles * 16 - 1) / (tiles * 16) * 16;
-}
+__device__ __forceinline__ int tile_height(int n, int tiles) { return (n + tiles * 16 - 1) / (tiles * 16) * 16; }
 
 // Workgroups go round the 8 dies in turn, so the tiles are dealt out in 8 contiguous runs, one to
 // a die: neighbouring tiles share weights or rows of a, which then are in that die's L2.
-template <int BM>
-__device__ __forceinline__ Tile find_tile(const GemmArgs& g, int col_tiles, uint32_t block) {
+__device__ __forceinline__ Tile find_tile(const GemmArgs& g, int bm, int col_tiles, uint32_t block) {
   const int lane = threadIdx.x & 63;
   Tile out{0, 0, 0, 0};
   int total = 0;
@@ -72,10 +68,10 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& g, int col_tiles, uint
     for (int e0 = 0; e0 < g.E; e0 += 64) {
       int first;
       const int n = group_rows(g, e0 + lane, first);
-      total += lane_int(wave_inclusive_add((n + BM - 1) / BM), 63);
+      total += lane_int(wave_inclusive_add((n + bm - 1) / bm), 63);
     }
   } else {
-    total = (g.M + BM - 1) / BM;
+    total = (g.M + bm - 1) / bm;
   }
   const uint32_t tiles = static_cast<uint32_t>(total) * col_tiles;
   const uint32_t per = (tiles + 7) / 8;
@@ -83,7 +79,7 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& g, int col_tiles, uint
   uint32_t t = (block % 8) * per + block / 8;
   if (t >= tiles) return out;
   if (!g.offsets) {
-    const int high = tile_height<BM>(g.M, total);
+    const int high = tile_height(g.M, total);
     out.col_tile = t / total;
     out.first = static_cast<int>(t % total) * high;
     out.rows = min(g.M - out.first, high);
@@ -92,7 +88,7 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& g, int col_tiles, uint
   for (int e0 = 0; e0 < g.E; e0 += 64) {
     int first;
     const int n = group_rows(g, e0 + lane, first);
-    const int mt = (n + BM - 1) / BM;
+    const int mt = (n + bm - 1) / bm;
     const int upto = wave_inclusive_add(mt);
     const uint32_t all = static_cast<uint32_t>(lane_int(upto, 63)) * col_tiles;
     if (t < all) {
@@ -100,11 +96,11 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& g, int col_tiles, uint
       const int l = __builtin_ctzll(hit);
       const int mt_l = lane_int(mt, l);
       const uint32_t in = t - static_cast<uint32_t>(lane_int(upto, l) - mt_l) * col_tiles;
-      const int n_l = lane_int(n, l), from = static_cast<int>(in % mt_l) * tile_height<BM>(n_l, mt_l);
+      const int n_l = lane_int(n, l), from = static_cast<int>(in % mt_l) * tile_height(n_l, mt_l);
       out.e = e0 + l;
       out.col_tile = in / mt_l;
       out.first = lane_int(first, l) + from;
-      out.rows = min(n_l - from, tile_height<BM>(n_l, mt_l));
+      out.rows = min(n_l - from, tile_height(n_l, mt_l));
       return out;
     }
     t -= all;
@@ -193,7 +189,7 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_gemm_stream_kernel(GemmArg
   __shared__ float part[kStreamWaves - 1][BN][BM + 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, piece = lane >> 4;
-  const Tile tile = find_tile<BM>(g, col_tiles, blockIdx.x);
+  const Tile tile = find_tile(g, BM, col_tiles, blockIdx.x);
   if (tile.rows <= 0) return;
   const int n0 = tile.col_tile * BN;
   const uint8_t* w_row[NT];
@@ -267,18 +263,23 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_gemm_stream_kernel(GemmArg
 }
 
 // ---- many rows ---------------------------------------------------------------------------------
-// A workgroup of four wavefronts holds a tile of up to 128 rows by 256 columns, each wavefront all
-// rows by 64 columns.  Every block of a is used by all four, so it goes through LDS (three stages,
-// filled by direct loads two blocks ahead); every block of weights is used by one wavefront only, so
-// it goes straight into that one's registers, one block ahead.  That leaves LDS with half the matrix
-// instructions' time.  The scales lie in LDS beside it.
-constexpr int kTileThreads = 256;
+// A workgroup of eight wavefronts, 2 by 4, holds a tile of up to 256 rows by 256 columns; each
+// wavefront has half the rows and 64 columns.  Both sides go through LDS, two stages of one block
+// each, filled by direct loads.  A wavefront holds its weights of a block in registers, so their
+// stage is free again after a few matrix instructions and the block after the next is asked for
+// then; rows of a (which other tiles keep in the die's L2) are asked for one block ahead.
+//
+// What bounds it: every CU draws (rows + 256) * 128 bytes of a block through its L2 path, about 36
+// bytes per cycle and CU, for rows * 256 * 128 products.  128-row tiles need 1.5 times the traffic of
+// 256-row ones for the same products.  (Weights are not loaded straight into registers: a matrix
+// operand wants neighbouring lanes on different rows, and the vector cache then takes one access for
+// every 16 bytes instead of one for 64.)
+constexpr int kTileThreads = 512, kTileWaves = kTileThreads / 64;
 constexpr int kTileN = 256, kWaveN = 4;      // kWaveN: 16-column pieces of a wavefront
-constexpr int kStages = 3;
-// Rows of the highest tile: its accumulators (4 registers for each 16 rows and 16 columns) fill half
-// the registers two wavefronts per SIMD leave; widening to fp16 needs 64 more for the weights.
+// Rows of the highest tile.  Accumulators fill half the registers; widening to fp16 needs the rest
+// for the weights.
 template <int DT>
-constexpr int kTileM = DT == MOE_DTYPE_F32 ? 64 : 128;
+constexpr int kTileM = DT == MOE_DTYPE_F32 ? 128 : 256;
 
 #define MOE_LDS __attribute__((address_space(3)))
 
@@ -292,59 +293,78 @@ __device__ __forceinline__ void lds_load16(uint32_t lds_addr, __amdgpu_buffer_rs
 
 // The scales of a and of the weights for kScaleBlocks blocks at a time, a row's fetched together: one
 // value per row and block would take as many L2 requests as half the weights do.
-constexpr int kScaleBlocks = 32;
+constexpr int kScaleBlocks = 16;
 
 template <int BM>
 struct TileLds {
-  uint8_t a[kStages][BM * kBlock];
+  uint8_t a[2][BM * kBlock];
+  uint8_t w[2][kTileN * kBlock];
   float a_scale[kScaleBlocks][BM];
   float w_scale[2][kScaleBlocks];   // of the tile's two 128-column halves
 };
 
-// A lane value the compiler recomputes addresses from instead of keeping them (they are 64 bits wide
-// and this kernel has no register to spare).
+// A lane value the compiler recomputes addresses from instead of keeping them.
 __device__ __forceinline__ uint32_t opaque(uint32_t v) {
   asm volatile("" : "+v"(v));
   return v;
 }
 
+// TM: pieces of 16 rows of one wavefront.
 template <int TM, int DT>
 __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, TileLds<kTileM<DT>>& lds) {
-  constexpr int BM = kTileM<DT>, kStageBytes = BM * kBlock;
   constexpr bool kFine = DT == MOE_DTYPE_F32;
+  constexpr int BM = kTileM<DT>;
+  using Lds = TileLds<BM>;
   using Op = Side<kFine>;
-  constexpr int kDma = TM / 2;      // direct loads of one stage per wavefront (1 KiB = 8 rows each)
+  // direct loads of one stage per wavefront, 1 KiB = 8 rows each
+  constexpr int kDmaA = (4 * TM + kTileWaves - 1) / kTileWaves, kDmaW = kTileN / 8 / kTileWaves;
+  constexpr int kSteps = TM * kWaveN, kLag = 2, kRelease = kWaveN;
+  static_assert(kDmaA <= kRelease && kRelease + kDmaW <= kSteps, "loads of a block fit between its products");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
   const int r = lane & 15, piece = lane >> 4;
-  const int nt0 = tile.col_tile * kTileN, n0 = nt0 + wave * 16 * kWaveN;
-  const uint8_t* w_base = g.w + (static_cast<int64_t>(tile.e) * g.N + nt0) * g.K;
-  uint32_t w_off[kWaveN];
-#pragma unroll
-  for (int j = 0; j < kWaveN; ++j)
-    w_off[j] = static_cast<uint32_t>(min(n0 + j * 16 + r, g.N - 1) - nt0) * g.K + piece * 16;
-  // Row `8 q + lane / 8` of the stage; its 16-byte piece c sits at slot c ^ (row % 8), so that the 16
-  // rows of a fragment read their pieces from all banks.  Offsets of 32 bits: from the tile's
-  // first row, or from the start of a if its rows are gathered (the entry point keeps those below 4 GiB).
-  const int chunk = (lane & 7) ^ (lane >> 3);
+  const int nt0 = tile.col_tile * kTileN, n0 = nt0 + wn * 16 * kWaveN, m0 = wm * 16 * TM;
+  // A stage's row is 128 bytes in 16-byte slots.  Row m of a has its piece c in slot c ^ (m % 8).  Lane r
+  // of piece j of the weights is column 16 (r / 4) + 4 j + r % 4 of the wavefront, so that a lane's
+  // results are 16 neighbouring columns; row n of them has its piece c in slot c ^ (n % 4 + 4 (n / 16 % 2)).
+  // Either way the 16 rows of a fragment read their pieces from all banks (slot c ^ (r % 8)).
+  // Offsets are 32 bits: of the weights from the tile's first row, of a from the tile's first row or
+  // from its start if rows are gathered (the entry point keeps those below 4 GiB).
+  const int sub = lane >> 3;
   const int64_t a_base = g.pairs ? 0 : source_row(g, tile.first);
   const auto a_rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.a + a_base * g.lda), 0, -1, 0x00027000);
-  uint32_t a_off[kDma];
+  const auto w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(g.w + (static_cast<int64_t>(tile.e) * g.N + nt0) * g.K), 0, -1, 0x00027000);
+  auto a_chunk = [&]() { return ((lane & 7) ^ sub) * 16; };
+  auto w_chunk = [&](int q) { return ((lane & 7) ^ ((sub & 3) | (q & 2) << 1)) * 16; };
+  uint32_t a_off[kDmaA], w_off[kDmaW];
 #pragma unroll
-  for (int q = 0; q < kDma; ++q) {
-    const int m = min((wave * kDma + q) * 8 + (lane >> 3), tile.rows - 1);
-    a_off[q] = static_cast<uint32_t>((source_row(g, tile.first + m) - a_base) * g.lda) + chunk * 16;
+  for (int q = 0; q < kDmaW; ++q)
+    w_off[q] = static_cast<uint32_t>(min((wave * kDmaW + q) * 8 + sub, g.N - 1 - nt0)) * g.K + w_chunk(q);
+#pragma unroll
+  for (int q = 0; q < kDmaA; ++q) {
+    const int m = min((wave * kDmaA + q) * 8 + sub, tile.rows - 1);
+    a_off[q] = static_cast<uint32_t>((source_row(g, tile.first + m) - a_base) * g.lda) + a_chunk();
   }
+
   const uint32_t lds_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS uint8_t*)&lds.a[0][0]));
+  const uint32_t w_at = lds_at + static_cast<uint32_t>(offsetof(Lds, w));
+  // Direct load q of a stage, from column `uniform` + `more` on.
+  auto load_a = [&](int q, int stage, uint32_t uniform, uint32_t more) {
+    lds_load16(lds_at + stage * (BM * kBlock) + (wave * kDmaA + q) * 1024, a_rsrc, a_off[q] + more, uniform);
+  };
+  auto load_w = [&](int q, int stage, uint32_t uniform, uint32_t more) {
+    lds_load16(w_at + stage * (kTileN * kBlock) + (wave * kDmaW + q) * 1024, w_rsrc, w_off[q] + more, uniform);
+  };
   // Scales of blocks [kb, kb + kScaleBlocks) into LDS; the caller waits and synchronises.  In
   // assembly, since the compiler would hold plain LDS stores until every direct load has landed.
   auto store_scales = [&](int kb) {
-    constexpr int kParts = kTileThreads / BM, kEach = kScaleBlocks / kParts;
+    constexpr int kParts = kTileThreads / BM, kEach = kScaleBlocks / kParts, kGroup = 4;
     const int tid = opaque(threadIdx.x);   // nothing of this is kept in registers between chunks
     const int row = tid / kParts, b0 = tid % kParts * kEach;
     const float* sa = g.a_scales + source_row(g, tile.first + min(row, tile.rows - 1)) * g.kb + kb;
     const int n = g.kb - kb;
-    const uint32_t to = lds_at + static_cast<uint32_t>(offsetof(TileLds<BM>, a_scale)) + (b0 * BM + row) * 4;
-    constexpr int kGroup = 8;   // in flight at once: the accumulators leave no registers for more
+    const uint32_t to = lds_at + static_cast<uint32_t>(offsetof(Lds, a_scale)) + (b0 * BM + row) * 4;
 #pragma unroll
     for (int i0 = 0; i0 < kEach; i0 += kGroup) {
       float v[kGroup];
@@ -359,48 +379,48 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
       const float w = g.w_scales[(static_cast<int64_t>(tile.e) * g.nb + min(nt0 / kBlock + half, g.nb - 1)) * g.kb + kb +
                                  min(i, n - 1)];
       asm volatile("ds_write_b32 %0, %1"
-                   : : "v"(lds_at + static_cast<uint32_t>(offsetof(TileLds<BM>, w_scale)) + tid * 4), "v"(w) : "memory");
+                   : : "v"(lds_at + static_cast<uint32_t>(offsetof(Lds, w_scale)) + tid * 4), "v"(w) : "memory");
     }
   };
 
-  auto load_w = [&](int kb, int j) {
-    union {
-      u32x4 half[2];
-      i32x8 all;
-    } u;
-    const uint8_t* p = w_base + static_cast<int64_t>(kb) * kBlock + opaque(w_off[j]);
-    u.half[0] = *reinterpret_cast<const u32x4*>(p);
-    u.half[1] = *reinterpret_cast<const u32x4*>(p + 64);
-    return u.all;
-  };
-  auto stage_a = [&](int kb, int stage, int q) {
-    lds_load16(lds_at + stage * kStageBytes + (wave * kDma + q) * 1024, a_rsrc, a_off[q], kb * kBlock);
-  };
   f32x4 acc[TM][kWaveN] = {};
-  const int a_at = r * kBlock + ((piece ^ (r & 7)) << 4);
-  // One block.  The next piece of a is read one row step ahead and results are added two matrix
-  // instructions after theirs, so that neither is waited for; `ahead(n)` issues the loads of the
-  // blocks to come between them.
-  auto multiply = [&](int kb, int stage, const Op (&w)[kWaveN], auto&& ahead) {
-    const uint8_t* a0 = &lds.a[stage][a_at];
-    const uint8_t* a1 = &lds.a[stage][a_at ^ 64];
-    const float* f = &lds.a_scale[kb % kScaleBlocks][r];
-    const float sw = lds.w_scale[wave >> 1][kb % kScaleBlocks];
-    auto read_a = [&](int i) {
-      union {
-        u32x4 half[2];
-        i32x8 all;
-      } u;
-      u.half[0] = *reinterpret_cast<const u32x4*>(a0 + i * 16 * kBlock);
-      u.half[1] = *reinterpret_cast<const u32x4*>(a1 + i * 16 * kBlock);
-      return u.all;
+  // this lane's first piece of a fragment; the other is at ^ 64
+  const int slot = (piece ^ (r & 7)) << 4;
+  const int a_frag = (m0 + r) * kBlock + slot, w_frag = (wn * 16 * kWaveN + (r >> 2) * 16 + (r & 3)) * kBlock + slot;
+  union Piece {
+    u32x4 half[2];
+    i32x8 all;
+  };
+  // One block of `left` columns.  The next piece of a is read one row step ahead and results are added
+  // two matrix instructions after theirs, so that neither is waited for; `between(n)` issues the loads
+  // of the blocks to come.
+  auto multiply = [&](int kb, int stage, auto tail, int left, auto&& between) {
+    const float* f = &lds.a_scale[kb % kScaleBlocks][m0 + r];
+    const float sw = lds.w_scale[wn >> 1][kb % kScaleBlocks];
+    auto read = [&](const uint8_t* side, int at) {
+      Piece u;
+      u.half[0] = *reinterpret_cast<const u32x4*>(side + at);
+      u.half[1] = *reinterpret_cast<const u32x4*>(side + (at ^ 64));
+      return u;
     };
-    constexpr int kSteps = TM * kWaveN, kLag = 2;
+    auto read_a = [&](int i) { return read(&lds.a[stage][i * 16 * kBlock], a_frag).all; };
     i32x8 a[2];
     float s[3];
     f32x4 p[kLag + 1];
     a[0] = read_a(0);
     s[0] = f[0] * sw;
+    i32x8 wv[kWaveN];
+#pragma unroll
+    for (int j = 0; j < kWaveN; ++j) {
+      Piece u = read(&lds.w[stage][j * 4 * kBlock], w_frag);
+      if (decltype(tail)::value) {   // pieces behind the row's end
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if ((piece + 4 * h) * 16 >= left) u.half[h] = u32x4{0, 0, 0, 0};
+      }
+      wv[j] = u.all;
+    }
+    const Op w[kWaveN] = {Op(wv[0]), Op(wv[1]), Op(wv[2]), Op(wv[3])};
     Op op(a[0]);
     auto add = [&](int n) {
 #pragma unroll
@@ -419,7 +439,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
       }
       p[n % (kLag + 1)] = mfma_block(w[j], op);
       __builtin_amdgcn_sched_barrier(0);
-      ahead(n);
+      between(n);
       if (n >= kLag) add(n - kLag);
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -427,99 +447,87 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
     for (int n = kSteps - kLag; n < kSteps; ++n) add(n);
   };
 
-  i32x8 w0[kWaveN], w1[kWaveN];
   const int full = g.K / kBlock, last = full - 1;
   if (full > 0) {
 #pragma unroll
-    for (int q = 0; q < kDma; ++q) stage_a(0, 0, q);
+    for (int q = 0; q < kDmaW; ++q) load_w(q, 0, 0, 0);
 #pragma unroll
-    for (int j = 0; j < kWaveN; ++j) w0[j] = load_w(0, j);
+    for (int q = 0; q < kDmaA; ++q) load_a(q, 0, 0, 0);
 #pragma unroll
-    for (int q = 0; q < kDma; ++q) stage_a(min(1, last), 1, q);
-    int stage = 0;
-    // The next block's weights and scales and the one after's rows of a are on their way while this
-    // one is multiplied.
-    auto step = [&](int kb, i32x8 (&now)[kWaveN], i32x8 (&next)[kWaveN]) {
+    for (int q = 0; q < kDmaW; ++q) load_w(q, 1, min(1, last) * kBlock, 0);
+    for (int kb = 0; kb <= last; ++kb) {
       if (kb % kScaleBlocks == 0) {
+        if (kb > 0) {   // every wavefront is through with the scales that are replaced
+          asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+          __builtin_amdgcn_s_barrier();
+        }
         store_scales(kb);
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kDma) : "memory");
-        __builtin_amdgcn_s_barrier();
       }
-      const int kn = min(kb + 1, last), stage_to = stage == 0 ? 2 : stage - 1;
-      const Op w[kWaveN] = {Op(now[0]), Op(now[1]), Op(now[2]), Op(now[3])};
-      if (kFine) __builtin_amdgcn_sched_barrier(0);
-      multiply(kb, stage, w, [&](int n) {
-        if (n < kWaveN) next[n] = load_w(kn, n);
-        else if (n < kWaveN + kDma) stage_a(min(kb + 2, last), stage_to, n - kWaveN);
-      });
-      // everything but the rows of a issued last has landed
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kDma) : "memory");
+      // this block has landed (the next one's weights may be in flight), and every wavefront is through
+      // with the stage that the next one's rows of a go to
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kDmaW) : "memory");
       __builtin_amdgcn_s_barrier();
-      stage = stage == 2 ? 0 : stage + 1;
-    };
-    int kb = 0;
-    if constexpr (kFine) {   // the widened weights are a copy: the next block's go where theirs came from
-      for (; kb <= last; ++kb) step(kb, w0, w0);
-    } else {
-      for (; kb < last; kb += 2) {
-        step(kb, w0, w1);
-        step(kb + 1, w1, w0);
-      }
-      if (kb == last) step(kb, w0, w1);
+      const int stage = kb & 1, next_a = min(kb + 1, last) * kBlock, next_w = min(kb + 2, last) * kBlock;
+      multiply(kb, stage, std::false_type{}, kBlock, [&](int n) {
+        if (n < kDmaA) load_a(n, stage ^ 1, next_a, 0);
+        if (n == kRelease) {   // every wavefront holds its weights of this block
+          asm volatile("" : : : "memory");
+          __builtin_amdgcn_s_barrier();
+        }
+        if (n >= kRelease && n < kRelease + kDmaW) load_w(n - kRelease, stage, next_w, 0);
+      });
     }
-    asm volatile("s_waitcnt vmcnt(0)" : : : "memory");   // the last stages' loads
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");   // the last stages' loads
     __builtin_amdgcn_s_barrier();
   }
-  // A short last block, not overlapped: the weights behind the row's end are zero, a's pieces there
-  // are read from the row's start (a row that holds NaN gives NaN anyway).
+  // A short last block, not overlapped.  Its pieces behind the row's end are read from the block's start;
+  // the weights are taken as zero there (a row of a that holds NaN gives NaN anyway).
   if (full < g.kb) {
+    const int left = g.K - full * kBlock;
     if (full % kScaleBlocks == 0) store_scales(full);
 #pragma unroll
-    for (int q = 0; q < kDma; ++q) {
-      const uint32_t at = full * kBlock + chunk * 16 < g.K ? full * kBlock : -(chunk * 16);
-      lds_load16(lds_at + (wave * kDma + q) * 1024, a_rsrc, a_off[q] + at, 0);
-    }
+    for (int q = 0; q < kDmaW; ++q) load_w(q, 0, full * kBlock, w_chunk(q) < left ? 0 : -w_chunk(q));
 #pragma unroll
-    for (int j = 0; j < kWaveN; ++j) w0[j] = load_pieces<true>(w_base + w_off[j] - piece * 16, full, g.K, piece);
+    for (int q = 0; q < kDmaA; ++q) load_a(q, 0, full * kBlock, a_chunk() < left ? 0 : -a_chunk());
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
     __builtin_amdgcn_s_barrier();
-    const Op w[kWaveN] = {Op(w0[0]), Op(w0[1]), Op(w0[2]), Op(w0[3])};
-    multiply(full, 0, w, [](int) {});
+    multiply(full, 0, std::true_type{}, left, [](int) {});
   }
 
   using T = typename Elem<DT>::T;
-  T* c = static_cast<T*>(g.c);
+  constexpr int kVec = kPerVec<DT>, kCols = 4 * kWaveN;   // a lane's neighbouring columns
+  const int n = n0 + piece * kCols;
+  T* c = static_cast<T*>(g.c) + n;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int m = i * 16 + r;
+    const int m = m0 + i * 16 + r;
     if (m < tile.rows) {
       T* row = c + static_cast<int64_t>(tile.first + m) * g.ldc;
 #pragma unroll
-      for (int j = 0; j < kWaveN; ++j) {
-        const int n = n0 + j * 16 + piece * 4;
-        struct __attribute__((packed, aligned(kElemSize<DT>))) Four { T e[4]; };
-        if (n + 4 <= g.N) {
-          *reinterpret_cast<Four*>(row + n) = Four{{static_cast<T>(acc[i][j][0]), static_cast<T>(acc[i][j][1]),
-                                                    static_cast<T>(acc[i][j][2]), static_cast<T>(acc[i][j][3])}};
-        } else {
+      for (int q = 0; q < kCols / kVec; ++q) {
+        float v[kVec];
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (n + v < g.N) row[n + v] = static_cast<T>(acc[i][j][v]);
-        }
+        for (int x = 0; x < kVec; ++x) v[x] = acc[i][(q * kVec + x) / 4][(q * kVec + x) % 4];
+        if (n + q * kVec < g.N) store_elems<DT>(row + q * kVec, g.N - n - q * kVec, v);
       }
     }
   }
 }
 
 template <int DT>
-__global__ __launch_bounds__(kTileThreads, 2) void fp8_gemm_tile_kernel(GemmArgs g, int col_tiles) {
+__global__ __launch_bounds__(kTileThreads, 2) void fp8_gemm_tile_kernel(GemmArgs g, int bm, int col_tiles) {
   __shared__ __align__(1024) TileLds<kTileM<DT>> lds;
-  const Tile tile = find_tile<kTileM<DT>>(g, col_tiles, blockIdx.x);
+  const Tile tile = find_tile(g, bm, col_tiles, blockIdx.x);
   if (tile.rows <= 0) return;
-  if (kTileM<DT> > 96 && tile.rows > 96) gemm_tile<kTileM<DT> / 16, DT>(g, tile, lds);
-  else if (kTileM<DT> > 64 && tile.rows > 64) gemm_tile<kTileM<DT> * 3 / 64, DT>(g, tile, lds);
-  else if (tile.rows > 32) gemm_tile<4, DT>(g, tile, lds);
-  else gemm_tile<2, DT>(g, tile, lds);
+  if constexpr (kTileM<DT> > 128) {
+    if (tile.rows > 224) return gemm_tile<8, DT>(g, tile, lds);
+    if (tile.rows > 192) return gemm_tile<7, DT>(g, tile, lds);
+    if (tile.rows > 160) return gemm_tile<6, DT>(g, tile, lds);
+    if (tile.rows > 128) return gemm_tile<5, DT>(g, tile, lds);
+  }
+  if (tile.rows > 96) return gemm_tile<4, DT>(g, tile, lds);
+  if (tile.rows > 64) return gemm_tile<3, DT>(g, tile, lds);
+  gemm_tile<2, DT>(g, tile, lds);
 }
 
 // Workgroups for tiles of BM by BN: every group with rows may have one partly filled row tile.
@@ -537,9 +545,10 @@ template <int DT>
 int launch_tile(const GemmArgs& g, hipStream_t stream) {
   uint32_t blocks;
   int col_tiles;
-  if (int rc = tile_blocks(g, kTileM<DT>, kTileN, &blocks, &col_tiles)) return rc;
+  const int bm = kTileM<DT>;
+  if (int rc = tile_blocks(g, bm, kTileN, &blocks, &col_tiles)) return rc;
   ProfileScope prof("fp8_gemm", stream);
-  hipLaunchKernelGGL(fp8_gemm_tile_kernel<DT>, dim3(blocks), dim3(kTileThreads), 0, stream, g, col_tiles);
+  hipLaunchKernelGGL(fp8_gemm_tile_kernel<DT>, dim3(blocks), dim3(kTileThreads), 0, stream, g, bm, col_tiles);
   return check_launch("fp8_gemm");
 }
 
