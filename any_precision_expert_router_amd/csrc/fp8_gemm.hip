@@ -58,33 +58,29 @@ __device__ __forceinline__ int group_rows(const GemmArgs& g, int e, int& first) 
 
 __device__ __forceinline__ int tile_height(int n, int tiles) { return (n + tiles * 16 - 1) / (tiles * 16) * 16; }
 
-// Workgroups go round the 8 dies in turn, so the tiles are dealt out in 8 contiguous runs, one to
-// a die: neighbouring tiles share weights or rows of a, which then are in that die's L2.
-__device__ __forceinline__ Tile find_tile(const GemmArgs& g, int bm, int col_tiles, uint32_t block) {
+// Row tiles of all groups together.
+__device__ __forceinline__ int count_row_tiles(const GemmArgs& g, int bm) {
+  if (!g.offsets) return (g.M + bm - 1) / bm;
   const int lane = threadIdx.x & 63;
-  Tile out{0, 0, 0, 0};
   int total = 0;
-  if (g.offsets) {
-    for (int e0 = 0; e0 < g.E; e0 += 64) {
-      int first;
-      const int n = group_rows(g, e0 + lane, first);
-      total += lane_int(wave_inclusive_add((n + bm - 1) / bm), 63);
-    }
-  } else {
-    total = (g.M + bm - 1) / bm;
+  for (int e0 = 0; e0 < g.E; e0 += 64) {
+    int first;
+    total += lane_int(wave_inclusive_add((group_rows(g, e0 + lane, first) + bm - 1) / bm), 63);
   }
-  const uint32_t tiles = static_cast<uint32_t>(total) * col_tiles;
-  const uint32_t per = (tiles + 7) / 8;
-  if (block / 8 >= per) return out;
-  uint32_t t = (block % 8) * per + block / 8;
-  if (t >= tiles) return out;
+  return total;
+}
+
+// Tile t < row_tiles * col_tiles; every lane of the wavefront takes part.
+__device__ __forceinline__ Tile tile_at(const GemmArgs& g, int bm, int row_tiles, int col_tiles, uint32_t t) {
+  Tile out{0, 0, 0, 0};
   if (!g.offsets) {
-    const int high = tile_height(g.M, total);
-    out.col_tile = t / total;
-    out.first = static_cast<int>(t % total) * high;
+    const int high = tile_height(g.M, row_tiles);
+    out.col_tile = t / row_tiles;
+    out.first = static_cast<int>(t % row_tiles) * high;
     out.rows = min(g.M - out.first, high);
     return out;
   }
+  const int lane = threadIdx.x & 63;
   for (int e0 = 0; e0 < g.E; e0 += 64) {
     int first;
     const int n = group_rows(g, e0 + lane, first);
@@ -106,6 +102,17 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs& g, int bm, int col_til
     t -= all;
   }
   return out;
+}
+
+// Workgroups go round the 8 dies in turn, so the tiles are dealt out in 8 contiguous runs, one to
+// a die: neighbouring tiles share weights or rows of a, which then are in that die's L2.  Die d has
+// tiles [first, end); its workgroups take them in turn.
+struct TileRun {
+  uint32_t first, end;
+};
+__device__ __forceinline__ TileRun die_tiles(uint32_t tiles, uint32_t die) {
+  const uint32_t per = (tiles + 7) / 8;
+  return {die * per, min((die + 1) * per, tiles)};
 }
 
 // Row of a behind row i of c.
@@ -189,7 +196,11 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_gemm_stream_kernel(GemmArg
   __shared__ float part[kStreamWaves - 1][BN][BM + 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, piece = lane >> 4;
-  const Tile tile = find_tile(g, BM, col_tiles, blockIdx.x);
+  const int row_tiles = count_row_tiles(g, BM);
+  const TileRun run = die_tiles(static_cast<uint32_t>(row_tiles) * col_tiles, blockIdx.x % 8);
+  const uint32_t t = run.first + blockIdx.x / 8;
+  if (t >= run.end) return;
+  const Tile tile = tile_at(g, BM, row_tiles, col_tiles, t);
   if (tile.rows <= 0) return;
   const int n0 = tile.col_tile * BN;
   const uint8_t* w_row[NT];
@@ -293,7 +304,7 @@ __device__ __forceinline__ void lds_load16(uint32_t lds_addr, __amdgpu_buffer_rs
 
 // The scales of a and of the weights for kScaleBlocks blocks at a time, a row's fetched together: one
 // value per row and block would take as many L2 requests as half the weights do.
-constexpr int kScaleBlocks = 16;
+constexpr int kScaleBlocks = 28;
 
 template <int BM>
 struct TileLds {
@@ -309,57 +320,86 @@ __device__ __forceinline__ uint32_t opaque(uint32_t v) {
   return v;
 }
 
+// What a wavefront loads of a tile: 1 KiB = 8 rows of a stage with each direct load, every eighth of
+// them.  A stage's row is 128 bytes in 16-byte slots.  Row m of a has its piece c in slot c ^ (m % 8).
+// Lane r of piece j of the weights is column 16 (r / 4) + 4 j + r % 4 of the wavefront, so that a lane's
+// results are 16 neighbouring columns; row n of them has its piece c in slot c ^ (n % 4 + 4 (n / 16 % 2)).
+// Either way the 16 rows of a fragment read their pieces from all banks (slot c ^ (r % 8)).
+// Offsets are 32 bits: of the weights from the tile's first row, of a from the tile's first row or
+// from its start if rows are gathered (the entry point keeps those below 4 GiB).
+template <int BM>
+struct Loader {
+  static constexpr int kA = BM / 8 / kTileWaves, kW = kTileN / 8 / kTileWaves;
+  __amdgpu_buffer_rsrc_t a_rsrc, w_rsrc;
+  uint32_t a_off[kA], w_off[kW];
+  int parts;     // of 8 rows the tile has
+  uint32_t a_at, w_at;
+
+  __device__ __forceinline__ static int lane() { return threadIdx.x & 63; }
+  __device__ __forceinline__ static int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+  __device__ __forceinline__ static uint32_t a_chunk() { return ((lane() & 7) ^ (lane() >> 3)) * 16; }
+  __device__ __forceinline__ static uint32_t w_chunk() {
+    return ((lane() & 7) ^ ((lane() >> 3 & 3) | (wave() >> 1 & 1) << 2)) * 16;
+  }
+
+  __device__ __forceinline__ void aim(const GemmArgs& g, const Tile& tile) {
+    const int nt0 = tile.col_tile * kTileN, sub = lane() >> 3;
+    w_rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.w + (static_cast<int64_t>(tile.e) * g.N + nt0) * g.K),
+                                               0, -1, 0x00027000);
+#pragma unroll
+    for (int q = 0; q < kW; ++q)
+      w_off[q] = static_cast<uint32_t>(min((q * kTileWaves + wave()) * 8 + sub, g.N - 1 - nt0)) * g.K + w_chunk();
+    const int64_t base = g.pairs ? 0 : source_row(g, tile.first);
+    a_rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.a + base * g.lda), 0, -1, 0x00027000);
+    parts = (tile.rows + 7) / 8;
+#pragma unroll
+    for (int q = 0; q < kA; ++q) {
+      const int m = min((q * kTileWaves + wave()) * 8 + sub, tile.rows - 1);
+      a_off[q] = static_cast<uint32_t>((source_row(g, tile.first + m) - base) * g.lda) + a_chunk();
+    }
+  }
+  // Direct load q of a stage, from column `uniform` + `more` on.
+  __device__ __forceinline__ void load_a(int q, int stage, uint32_t uniform, uint32_t more = 0) const {
+    if (q * kTileWaves + wave() < parts)
+      lds_load16(a_at + stage * (BM * kBlock) + (q * kTileWaves + wave()) * 1024, a_rsrc, a_off[q] + more, uniform);
+  }
+  __device__ __forceinline__ void load_w(int q, int stage, uint32_t uniform, uint32_t more = 0) const {
+    lds_load16(w_at + stage * (kTileN * kBlock) + (q * kTileWaves + wave()) * 1024, w_rsrc, w_off[q] + more, uniform);
+  }
+  // The first block and the weights of the second; multiplying starts with these on their way.
+  __device__ __forceinline__ void start(const GemmArgs& g) const {
+    const int full = g.K / kBlock;
+    if (full == 0) return;
+#pragma unroll
+    for (int q = 0; q < kW; ++q) load_w(q, 0, 0);
+#pragma unroll
+    for (int q = 0; q < kA; ++q) load_a(q, 0, 0);
+#pragma unroll
+    for (int q = 0; q < kW; ++q) load_w(q, 1, min(1, full - 1) * kBlock);
+  }
+};
+
+// One tile whose first loads are on their way; leaves those of `next` (if it has rows) on theirs.
 // TM: pieces of 16 rows of one wavefront.
 template <int TM, int DT>
-__device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, TileLds<kTileM<DT>>& lds) {
+__device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, const Tile& next, Loader<kTileM<DT>>& from,
+                                          TileLds<kTileM<DT>>& lds) {
   constexpr bool kFine = DT == MOE_DTYPE_F32;
   constexpr int BM = kTileM<DT>;
   using Lds = TileLds<BM>;
   using Op = Side<kFine>;
-  // direct loads of one stage per wavefront, 1 KiB = 8 rows each
-  constexpr int kDmaA = (4 * TM + kTileWaves - 1) / kTileWaves, kDmaW = kTileN / 8 / kTileWaves;
+  constexpr int kDmaA = Loader<BM>::kA, kDmaW = Loader<BM>::kW;
   constexpr int kSteps = TM * kWaveN, kLag = 2, kRelease = kWaveN;
   static_assert(kDmaA <= kRelease && kRelease + kDmaW <= kSteps, "loads of a block fit between its products");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int r = lane & 15, piece = lane >> 4;
   const int nt0 = tile.col_tile * kTileN, n0 = nt0 + wn * 16 * kWaveN, m0 = wm * 16 * TM;
-  // A stage's row is 128 bytes in 16-byte slots.  Row m of a has its piece c in slot c ^ (m % 8).  Lane r
-  // of piece j of the weights is column 16 (r / 4) + 4 j + r % 4 of the wavefront, so that a lane's
-  // results are 16 neighbouring columns; row n of them has its piece c in slot c ^ (n % 4 + 4 (n / 16 % 2)).
-  // Either way the 16 rows of a fragment read their pieces from all banks (slot c ^ (r % 8)).
-  // Offsets are 32 bits: of the weights from the tile's first row, of a from the tile's first row or
-  // from its start if rows are gathered (the entry point keeps those below 4 GiB).
-  const int sub = lane >> 3;
-  const int64_t a_base = g.pairs ? 0 : source_row(g, tile.first);
-  const auto a_rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.a + a_base * g.lda), 0, -1, 0x00027000);
-  const auto w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(g.w + (static_cast<int64_t>(tile.e) * g.N + nt0) * g.K), 0, -1, 0x00027000);
-  auto a_chunk = [&]() { return ((lane & 7) ^ sub) * 16; };
-  auto w_chunk = [&](int q) { return ((lane & 7) ^ ((sub & 3) | (q & 2) << 1)) * 16; };
-  uint32_t a_off[kDmaA], w_off[kDmaW];
-#pragma unroll
-  for (int q = 0; q < kDmaW; ++q)
-    w_off[q] = static_cast<uint32_t>(min((wave * kDmaW + q) * 8 + sub, g.N - 1 - nt0)) * g.K + w_chunk(q);
-#pragma unroll
-  for (int q = 0; q < kDmaA; ++q) {
-    const int m = min((wave * kDmaA + q) * 8 + sub, tile.rows - 1);
-    a_off[q] = static_cast<uint32_t>((source_row(g, tile.first + m) - a_base) * g.lda) + a_chunk();
-  }
-
-  const uint32_t lds_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS uint8_t*)&lds.a[0][0]));
-  const uint32_t w_at = lds_at + static_cast<uint32_t>(offsetof(Lds, w));
-  // Direct load q of a stage, from column `uniform` + `more` on.
-  auto load_a = [&](int q, int stage, uint32_t uniform, uint32_t more) {
-    lds_load16(lds_at + stage * (BM * kBlock) + (wave * kDmaA + q) * 1024, a_rsrc, a_off[q] + more, uniform);
-  };
-  auto load_w = [&](int q, int stage, uint32_t uniform, uint32_t more) {
-    lds_load16(w_at + stage * (kTileN * kBlock) + (wave * kDmaW + q) * 1024, w_rsrc, w_off[q] + more, uniform);
-  };
+  const uint32_t lds_at = from.a_at;
   // Scales of blocks [kb, kb + kScaleBlocks) into LDS; the caller waits and synchronises.  In
   // assembly, since the compiler would hold plain LDS stores until every direct load has landed.
   auto store_scales = [&](int kb) {
-    constexpr int kParts = kTileThreads / BM, kEach = kScaleBlocks / kParts, kGroup = 4;
+    constexpr int kParts = kTileThreads / BM, kEach = kScaleBlocks / kParts, kGroup = 7;
     const int tid = opaque(threadIdx.x);   // nothing of this is kept in registers between chunks
     const int row = tid / kParts, b0 = tid % kParts * kEach;
     const float* sa = g.a_scales + source_row(g, tile.first + min(row, tile.rows - 1)) * g.kb + kb;
@@ -394,7 +434,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
   // One block of `left` columns.  The next piece of a is read one row step ahead and results are added
   // two matrix instructions after theirs, so that neither is waited for; `between(n)` issues the loads
   // of the blocks to come.
-  auto multiply = [&](int kb, int stage, auto tail, int left, auto&& between) {
+  auto multiply = [&](int kb, int stage, auto tail, uint32_t left, auto&& between) {
     const float* f = &lds.a_scale[kb % kScaleBlocks][m0 + r];
     const float sw = lds.w_scale[wn >> 1][kb % kScaleBlocks];
     auto read = [&](const uint8_t* side, int at) {
@@ -449,12 +489,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
 
   const int full = g.K / kBlock, last = full - 1;
   if (full > 0) {
-#pragma unroll
-    for (int q = 0; q < kDmaW; ++q) load_w(q, 0, 0, 0);
-#pragma unroll
-    for (int q = 0; q < kDmaA; ++q) load_a(q, 0, 0, 0);
-#pragma unroll
-    for (int q = 0; q < kDmaW; ++q) load_w(q, 1, min(1, last) * kBlock, 0);
     for (int kb = 0; kb <= last; ++kb) {
       if (kb % kScaleBlocks == 0) {
         if (kb > 0) {   // every wavefront is through with the scales that are replaced
@@ -469,12 +503,12 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
       __builtin_amdgcn_s_barrier();
       const int stage = kb & 1, next_a = min(kb + 1, last) * kBlock, next_w = min(kb + 2, last) * kBlock;
       multiply(kb, stage, std::false_type{}, kBlock, [&](int n) {
-        if (n < kDmaA) load_a(n, stage ^ 1, next_a, 0);
+        if (n < kDmaA) from.load_a(n, stage ^ 1, next_a);
         if (n == kRelease) {   // every wavefront holds its weights of this block
           asm volatile("" : : : "memory");
           __builtin_amdgcn_s_barrier();
         }
-        if (n >= kRelease && n < kRelease + kDmaW) load_w(n - kRelease, stage, next_w, 0);
+        if (n >= kRelease && n < kRelease + kDmaW) from.load_w(n - kRelease, stage, next_w);
       });
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");   // the last stages' loads
@@ -483,15 +517,23 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
   // A short last block, not overlapped.  Its pieces behind the row's end are read from the block's start;
   // the weights are taken as zero there (a row of a that holds NaN gives NaN anyway).
   if (full < g.kb) {
-    const int left = g.K - full * kBlock;
+    const uint32_t left = g.K - full * kBlock;
     if (full % kScaleBlocks == 0) store_scales(full);
 #pragma unroll
-    for (int q = 0; q < kDmaW; ++q) load_w(q, 0, full * kBlock, w_chunk(q) < left ? 0 : -w_chunk(q));
+    for (int q = 0; q < kDmaW; ++q) from.load_w(q, 0, full * kBlock, from.w_chunk() < left ? 0 : -from.w_chunk());
 #pragma unroll
-    for (int q = 0; q < kDmaA; ++q) load_a(q, 0, full * kBlock, a_chunk() < left ? 0 : -a_chunk());
+    for (int q = 0; q < kDmaA; ++q) from.load_a(q, 0, full * kBlock, from.a_chunk() < left ? 0 : -from.a_chunk());
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
     __builtin_amdgcn_s_barrier();
     multiply(full, 0, std::true_type{}, left, [](int) {});
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    __builtin_amdgcn_s_barrier();
+  }
+
+  // The next tile's loads go out before this one's results.
+  if (next.rows > 0) {
+    from.aim(g, next);
+    from.start(g);
   }
 
   using T = typename Elem<DT>::T;
@@ -516,18 +558,33 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, T
 
 template <int DT>
 __global__ __launch_bounds__(kTileThreads, 2) void fp8_gemm_tile_kernel(GemmArgs g, int bm, int col_tiles) {
-  __shared__ __align__(1024) TileLds<kTileM<DT>> lds;
-  const Tile tile = find_tile(g, bm, col_tiles, blockIdx.x);
-  if (tile.rows <= 0) return;
-  if constexpr (kTileM<DT> > 128) {
-    if (tile.rows > 224) return gemm_tile<8, DT>(g, tile, lds);
-    if (tile.rows > 192) return gemm_tile<7, DT>(g, tile, lds);
-    if (tile.rows > 160) return gemm_tile<6, DT>(g, tile, lds);
-    if (tile.rows > 128) return gemm_tile<5, DT>(g, tile, lds);
+  constexpr int BM = kTileM<DT>;
+  __shared__ __align__(1024) TileLds<BM> lds;
+  const int row_tiles = count_row_tiles(g, bm);
+  const TileRun run = die_tiles(static_cast<uint32_t>(row_tiles) * col_tiles, blockIdx.x % 8);
+  uint32_t t = run.first + blockIdx.x / 8;
+  if (t >= run.end) return;
+  Loader<BM> from;
+  from.a_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS uint8_t*)&lds.a[0][0]));
+  from.w_at = from.a_at + static_cast<uint32_t>(offsetof(TileLds<BM>, w));
+  Tile tile = tile_at(g, bm, row_tiles, col_tiles, t);
+  from.aim(g, tile);
+  from.start(g);
+  while (tile.rows > 0) {
+    t += gridDim.x / 8;
+    Tile next{0, 0, 0, 0};
+    if (t < run.end) next = tile_at(g, bm, row_tiles, col_tiles, t);
+    if constexpr (BM > 128) {
+      if (tile.rows > 224) gemm_tile<8, DT>(g, tile, next, from, lds);
+      else if (tile.rows > 192) gemm_tile<7, DT>(g, tile, next, from, lds);
+      else if (tile.rows > 160) gemm_tile<6, DT>(g, tile, next, from, lds);
+      else if (tile.rows > 128) gemm_tile<5, DT>(g, tile, next, from, lds);
+    }
+    if (tile.rows <= 64) gemm_tile<2, DT>(g, tile, next, from, lds);
+    else if (tile.rows <= 96) gemm_tile<3, DT>(g, tile, next, from, lds);
+    else if (tile.rows <= 128) gemm_tile<4, DT>(g, tile, next, from, lds);
+    tile = next;
   }
-  if (tile.rows > 96) return gemm_tile<4, DT>(g, tile, lds);
-  if (tile.rows > 64) return gemm_tile<3, DT>(g, tile, lds);
-  gemm_tile<2, DT>(g, tile, lds);
 }
 
 // Workgroups for tiles of BM by BN: every group with rows may have one partly filled row tile.
@@ -547,8 +604,10 @@ int launch_tile(const GemmArgs& g, hipStream_t stream) {
   int col_tiles;
   const int bm = kTileM<DT>;
   if (int rc = tile_blocks(g, bm, kTileN, &blocks, &col_tiles)) return rc;
+  // LDS holds one workgroup per compute unit: each takes tiles until its die's run is done
+  const uint32_t grid = min(blocks, static_cast<uint32_t>((device_cu_count() + 7) / 8 * 8));
   ProfileScope prof("fp8_gemm", stream);
-  hipLaunchKernelGGL(fp8_gemm_tile_kernel<DT>, dim3(blocks), dim3(kTileThreads), 0, stream, g, bm, col_tiles);
+  hipLaunchKernelGGL(fp8_gemm_tile_kernel<DT>, dim3(grid), dim3(kTileThreads), 0, stream, g, bm, col_tiles);
   return check_launch("fp8_gemm");
 }
 
