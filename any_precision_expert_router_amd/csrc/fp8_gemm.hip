@@ -304,13 +304,13 @@ __device__ __forceinline__ void lds_load16(uint32_t lds_addr, __amdgpu_buffer_rs
 
 // The scales of a and of the weights for kScaleBlocks blocks at a time, a row's fetched together: one
 // value per row and block would take as many L2 requests as half the weights do.
-constexpr int kScaleBlocks = 28;
+constexpr int kScaleBlocks = 28, kScalePitch = kScaleBlocks + 1;   // odd: 16 rows' scales are in 16 banks
 
 template <int BM>
 struct TileLds {
   uint8_t a[2][BM * kBlock];
   uint8_t w[2][kTileN * kBlock];
-  float a_scale[kScaleBlocks][BM];
+  float a_scale[BM][kScalePitch];
   float w_scale[2][kScaleBlocks];   // of the tile's two 128-column halves
 };
 
@@ -322,14 +322,16 @@ __device__ __forceinline__ uint32_t opaque(uint32_t v) {
 
 // What a wavefront loads of a tile: 1 KiB = 8 rows of a stage with each direct load, every eighth of
 // them.  A stage's row is 128 bytes in 16-byte slots.  Row m of a has its piece c in slot c ^ (m % 8).
-// Lane r of piece j of the weights is column 16 (r / 4) + 4 j + r % 4 of the wavefront, so that a lane's
-// results are 16 neighbouring columns; row n of them has its piece c in slot c ^ (n % 4 + 4 (n / 16 % 2)).
-// Either way the 16 rows of a fragment read their pieces from all banks (slot c ^ (r % 8)).
+// The weights' rows are dealt to the lanes so that a lane's results are neighbouring columns; row n of
+// them has its piece c in slot c ^ (n % 4 + 4 (n / (4 COLS) % 2)).  Either way the 16 rows of a fragment
+// read their pieces from all banks (slot c ^ (r % 8)).
 // Offsets are 32 bits: of the weights from the tile's first row, of a from the tile's first row or
 // from its start if rows are gathered (the entry point keeps those below 4 GiB).
-template <int BM>
+//
+// COLS: 16-column pieces of a wavefront.  Its lane r of piece j is column 4 COLS (r / 4) + 4 j + r % 4.
+template <int BM, int COLS>
 struct Loader {
-  static constexpr int kA = BM / 8 / kTileWaves, kW = kTileN / 8 / kTileWaves;
+  static constexpr int kA = (BM / 8 + kTileWaves - 1) / kTileWaves, kW = kTileN / 8 / kTileWaves;
   __amdgpu_buffer_rsrc_t a_rsrc, w_rsrc;
   uint32_t a_off[kA], w_off[kW];
   int parts;     // of 8 rows the tile has
@@ -339,7 +341,8 @@ struct Loader {
   __device__ __forceinline__ static int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
   __device__ __forceinline__ static uint32_t a_chunk() { return ((lane() & 7) ^ (lane() >> 3)) * 16; }
   __device__ __forceinline__ static uint32_t w_chunk() {
-    return ((lane() & 7) ^ ((lane() >> 3 & 3) | (wave() >> 1 & 1) << 2)) * 16;
+    static_assert(COLS == 2 || COLS == 4, "4 COLS is 8 or 16 rows: one or two wavefronts' parts");
+    return ((lane() & 7) ^ ((lane() >> 3 & 3) | ((COLS == 4 ? wave() >> 1 : wave()) & 1) << 2)) * 16;
   }
 
   __device__ __forceinline__ void aim(const GemmArgs& g, const Tile& tile) {
@@ -354,73 +357,97 @@ struct Loader {
     parts = (tile.rows + 7) / 8;
 #pragma unroll
     for (int q = 0; q < kA; ++q) {
-      const int m = min((q * kTileWaves + wave()) * 8 + sub, tile.rows - 1);
+      const int m = min((q * kTileWaves + wave()) % (BM / 8) * 8 + sub, tile.rows - 1);
       a_off[q] = static_cast<uint32_t>((source_row(g, tile.first + m) - base) * g.lda) + a_chunk();
     }
   }
   // Direct load q of a stage, from column `uniform` + `more` on.
   __device__ __forceinline__ void load_a(int q, int stage, uint32_t uniform, uint32_t more = 0) const {
-    if (q * kTileWaves + wave() < parts)
-      lds_load16(a_at + stage * (BM * kBlock) + (q * kTileWaves + wave()) * 1024, a_rsrc, a_off[q] + more, uniform);
+    const int part = (q * kTileWaves + wave()) % (BM / 8);   // few rows: some parts twice, the same bytes
+    if (BM < 64 || part < parts)
+      lds_load16(a_at + stage * (BM * kBlock) + part * 1024, a_rsrc, a_off[q] + more, uniform);
   }
   __device__ __forceinline__ void load_w(int q, int stage, uint32_t uniform, uint32_t more = 0) const {
     lds_load16(w_at + stage * (kTileN * kBlock) + (q * kTileWaves + wave()) * 1024, w_rsrc, w_off[q] + more, uniform);
   }
-  // The first block and the weights of the second; multiplying starts with these on their way.
-  __device__ __forceinline__ void start(const GemmArgs& g) const {
-    const int full = g.K / kBlock;
-    if (full == 0) return;
-#pragma unroll
-    for (int q = 0; q < kW; ++q) load_w(q, 0, 0);
-#pragma unroll
-    for (int q = 0; q < kA; ++q) load_a(q, 0, 0);
-#pragma unroll
-    for (int q = 0; q < kW; ++q) load_w(q, 1, min(1, full - 1) * kBlock);
-  }
 };
+
+// Scales of blocks [kb, kb + kScaleBlocks) into LDS ([row][block] of a, [half][block] of the weights);
+// the caller waits and synchronises.  In assembly, since the compiler would hold plain LDS stores
+// until every direct load has landed.
+template <int BM>
+__device__ __forceinline__ void store_scales(const GemmArgs& g, const Tile& tile, int kb, uint32_t a_to, uint32_t w_to) {
+  constexpr int kEach = (BM * kScaleBlocks + kTileThreads - 1) / kTileThreads, kGroup = kEach % 7 ? kEach : 7;
+  const int tid = opaque(threadIdx.x);   // nothing of this is kept in registers between chunks
+  const int n = g.kb - kb;
+#pragma unroll
+  for (int i0 = 0; i0 < kEach; i0 += kGroup) {
+    float v[kGroup];
+    uint32_t to[kGroup];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      const int x = min(tid + (i0 + i) * kTileThreads, BM * kScaleBlocks - 1), row = x / kScaleBlocks, b = x % kScaleBlocks;
+      v[i] = g.a_scales[source_row(g, tile.first + min(row, tile.rows - 1)) * g.kb + kb + min(b, n - 1)];
+      to[i] = a_to + (row * kScalePitch + b) * 4;
+    }
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) asm volatile("ds_write_b32 %0, %1" : : "v"(to[i]), "v"(v[i]) : "memory");
+  }
+  if (tid < 2 * kScaleBlocks) {
+    const int half = tid / kScaleBlocks, i = tid % kScaleBlocks, nb = min(tile.col_tile * (kTileN / kBlock) + half, g.nb - 1);
+    const float w = g.w_scales[(static_cast<int64_t>(tile.e) * g.nb + nb) * g.kb + kb + min(i, n - 1)];
+    asm volatile("ds_write_b32 %0, %1" : : "v"(w_to + tid * 4), "v"(w) : "memory");
+  }
+}
+
+// Results of 16 rows (lane r's row is `m`) and COLS pieces: a lane's 4 COLS neighbouring columns, from n on.
+template <int COLS, int DT>
+__device__ __forceinline__ void store_row(const GemmArgs& g, const Tile& tile, int m, int n, const f32x4 (&acc)[COLS]) {
+  using T = typename Elem<DT>::T;
+  constexpr int kVec = kPerVec<DT>;
+  if (m >= tile.rows) return;
+  T* row = static_cast<T*>(g.c) + static_cast<int64_t>(tile.first + m) * g.ldc + n;
+#pragma unroll
+  for (int q = 0; q < 4 * COLS / kVec; ++q) {
+    float v[kVec];
+#pragma unroll
+    for (int x = 0; x < kVec; ++x) v[x] = acc[(q * kVec + x) / 4][(q * kVec + x) % 4];
+    if (n + q * kVec < g.N) store_elems<DT>(row + q * kVec, g.N - n - q * kVec, v);
+  }
+}
+
+// A tile's first block and the weights of its second: multiplying starts with these on their way.
+template <int BM>
+__device__ __forceinline__ void start_tile(const GemmArgs& g, const Loader<BM, kWaveN>& from) {
+  const int full = g.K / kBlock;
+  if (full == 0) return;
+#pragma unroll
+  for (int q = 0; q < from.kW; ++q) from.load_w(q, 0, 0);
+#pragma unroll
+  for (int q = 0; q < from.kA; ++q) from.load_a(q, 0, 0);
+#pragma unroll
+  for (int q = 0; q < from.kW; ++q) from.load_w(q, 1, min(1, full - 1) * kBlock);
+}
 
 // One tile whose first loads are on their way; leaves those of `next` (if it has rows) on theirs.
 // TM: pieces of 16 rows of one wavefront.
 template <int TM, int DT>
-__device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, const Tile& next, Loader<kTileM<DT>>& from,
+__device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, const Tile& next, Loader<kTileM<DT>, kWaveN>& from,
                                           TileLds<kTileM<DT>>& lds) {
   constexpr bool kFine = DT == MOE_DTYPE_F32;
   constexpr int BM = kTileM<DT>;
   using Lds = TileLds<BM>;
   using Op = Side<kFine>;
-  constexpr int kDmaA = Loader<BM>::kA, kDmaW = Loader<BM>::kW;
+  constexpr int kDmaA = Loader<BM, kWaveN>::kA, kDmaW = Loader<BM, kWaveN>::kW;
   constexpr int kSteps = TM * kWaveN, kLag = 2, kRelease = kWaveN;
   static_assert(kDmaA <= kRelease && kRelease + kDmaW <= kSteps, "loads of a block fit between its products");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int r = lane & 15, piece = lane >> 4;
   const int nt0 = tile.col_tile * kTileN, n0 = nt0 + wn * 16 * kWaveN, m0 = wm * 16 * TM;
-  const uint32_t lds_at = from.a_at;
-  // Scales of blocks [kb, kb + kScaleBlocks) into LDS; the caller waits and synchronises.  In
-  // assembly, since the compiler would hold plain LDS stores until every direct load has landed.
-  auto store_scales = [&](int kb) {
-    constexpr int kParts = kTileThreads / BM, kEach = kScaleBlocks / kParts, kGroup = 7;
-    const int tid = opaque(threadIdx.x);   // nothing of this is kept in registers between chunks
-    const int row = tid / kParts, b0 = tid % kParts * kEach;
-    const float* sa = g.a_scales + source_row(g, tile.first + min(row, tile.rows - 1)) * g.kb + kb;
-    const int n = g.kb - kb;
-    const uint32_t to = lds_at + static_cast<uint32_t>(offsetof(Lds, a_scale)) + (b0 * BM + row) * 4;
-#pragma unroll
-    for (int i0 = 0; i0 < kEach; i0 += kGroup) {
-      float v[kGroup];
-#pragma unroll
-      for (int i = 0; i < kGroup; ++i) v[i] = sa[min(b0 + i0 + i, n - 1)];
-#pragma unroll
-      for (int i = 0; i < kGroup; ++i)
-        asm volatile("ds_write_b32 %0, %1 offset:%2" : : "v"(to), "v"(v[i]), "n"((i0 + i) * BM * 4) : "memory");
-    }
-    if (tid < 2 * kScaleBlocks) {
-      const int half = tid / kScaleBlocks, i = tid % kScaleBlocks;
-      const float w = g.w_scales[(static_cast<int64_t>(tile.e) * g.nb + min(nt0 / kBlock + half, g.nb - 1)) * g.kb + kb +
-                                 min(i, n - 1)];
-      asm volatile("ds_write_b32 %0, %1"
-                   : : "v"(lds_at + static_cast<uint32_t>(offsetof(Lds, w_scale)) + tid * 4), "v"(w) : "memory");
-    }
+  auto scales = [&](int kb) {
+    store_scales<BM>(g, tile, kb, from.a_at + static_cast<uint32_t>(offsetof(Lds, a_scale)),
+                     from.a_at + static_cast<uint32_t>(offsetof(Lds, w_scale)));
   };
 
   f32x4 acc[TM][kWaveN] = {};
@@ -435,7 +462,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
   // two matrix instructions after theirs, so that neither is waited for; `between(n)` issues the loads
   // of the blocks to come.
   auto multiply = [&](int kb, int stage, auto tail, uint32_t left, auto&& between) {
-    const float* f = &lds.a_scale[kb % kScaleBlocks][m0 + r];
+    const float* f = &lds.a_scale[m0 + r][kb % kScaleBlocks];
     const float sw = lds.w_scale[wn >> 1][kb % kScaleBlocks];
     auto read = [&](const uint8_t* side, int at) {
       Piece u;
@@ -474,7 +501,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
         op = Op(a[i & 1]);
         if (i + 1 < TM) {
           a[(i + 1) & 1] = read_a(i + 1);
-          s[(i + 1) % 3] = f[(i + 1) * 16] * sw;
+          s[(i + 1) % 3] = f[(i + 1) * 16 * kScalePitch] * sw;
         }
       }
       p[n % (kLag + 1)] = mfma_block(w[j], op);
@@ -495,7 +522,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
           asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
           __builtin_amdgcn_s_barrier();
         }
-        store_scales(kb);
+        scales(kb);
       }
       // this block has landed (the next one's weights may be in flight), and every wavefront is through
       // with the stage that the next one's rows of a go to
@@ -518,7 +545,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
   // the weights are taken as zero there (a row of a that holds NaN gives NaN anyway).
   if (full < g.kb) {
     const uint32_t left = g.K - full * kBlock;
-    if (full % kScaleBlocks == 0) store_scales(full);
+    if (full % kScaleBlocks == 0) scales(full);
 #pragma unroll
     for (int q = 0; q < kDmaW; ++q) from.load_w(q, 0, full * kBlock, from.w_chunk() < left ? 0 : -from.w_chunk());
 #pragma unroll
@@ -533,27 +560,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
   // The next tile's loads go out before this one's results.
   if (next.rows > 0) {
     from.aim(g, next);
-    from.start(g);
+    start_tile(g, from);
   }
 
-  using T = typename Elem<DT>::T;
-  constexpr int kVec = kPerVec<DT>, kCols = 4 * kWaveN;   // a lane's neighbouring columns
-  const int n = n0 + piece * kCols;
-  T* c = static_cast<T*>(g.c) + n;
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int m = m0 + i * 16 + r;
-    if (m < tile.rows) {
-      T* row = c + static_cast<int64_t>(tile.first + m) * g.ldc;
-#pragma unroll
-      for (int q = 0; q < kCols / kVec; ++q) {
-        float v[kVec];
-#pragma unroll
-        for (int x = 0; x < kVec; ++x) v[x] = acc[i][(q * kVec + x) / 4][(q * kVec + x) % 4];
-        if (n + q * kVec < g.N) store_elems<DT>(row + q * kVec, g.N - n - q * kVec, v);
-      }
-    }
-  }
+  for (int i = 0; i < TM; ++i) store_row<kWaveN, DT>(g, tile, m0 + i * 16 + r, n0 + piece * 4 * kWaveN, acc[i]);
 }
 
 template <int DT>
@@ -564,12 +575,12 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_gemm_tile_kernel(GemmArgs
   const TileRun run = die_tiles(static_cast<uint32_t>(row_tiles) * col_tiles, blockIdx.x % 8);
   uint32_t t = run.first + blockIdx.x / 8;
   if (t >= run.end) return;
-  Loader<BM> from;
+  Loader<BM, kWaveN> from;
   from.a_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS uint8_t*)&lds.a[0][0]));
   from.w_at = from.a_at + static_cast<uint32_t>(offsetof(TileLds<BM>, w));
   Tile tile = tile_at(g, bm, row_tiles, col_tiles, t);
   from.aim(g, tile);
-  from.start(g);
+  start_tile(g, from);
   while (tile.rows > 0) {
     t += gridDim.x / 8;
     Tile next{0, 0, 0, 0};
@@ -587,6 +598,146 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_gemm_tile_kernel(GemmArgs
   }
 }
 
+// ---- few rows to a group, many weights ----------------------------------------------------------
+// Tiles of up to 32 rows by 256 columns, each of the eight wavefronts all rows by 32 columns.  The
+// weights are read once and bound it, so the stages are small enough for kFewStages of them and the
+// loads run kFewStages - 1 blocks ahead.
+constexpr int kFewM = 32, kFewStages = 4, kFewN = 2;
+
+struct FewLds {
+  uint8_t a[kFewStages][kFewM * kBlock];
+  uint8_t w[kFewStages][kTileN * kBlock];
+  float a_scale[kFewM][kScalePitch];
+  float w_scale[2][kScaleBlocks];
+};
+using FewLoader = Loader<kFewM, kFewN>;
+
+__device__ __forceinline__ void few_load(const FewLoader& from, int stage, uint32_t uniform) {
+#pragma unroll
+  for (int q = 0; q < from.kW; ++q) from.load_w(q, stage, uniform);
+  from.load_a(0, stage, uniform);
+}
+__device__ __forceinline__ void few_start(const GemmArgs& g, const FewLoader& from) {
+  const int full = g.K / kBlock;
+  if (full == 0) return;
+#pragma unroll
+  for (int d = 0; d < kFewStages - 1; ++d) few_load(from, d, min(d, full - 1) * kBlock);
+}
+
+template <int TM, int DT>
+__device__ __forceinline__ void few_tile(const GemmArgs& g, const Tile& tile, const Tile& next, FewLoader& from, FewLds& lds) {
+  using Op = Side<DT == MOE_DTYPE_F32>;
+  constexpr int kLoads = FewLoader::kW + 1;
+  static_assert(FewLoader::kA == 1, "one direct load of a and kW of the weights to a stage");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, piece = lane >> 4;
+  auto scales = [&](int kb) {
+    store_scales<kFewM>(g, tile, kb, from.a_at + static_cast<uint32_t>(offsetof(FewLds, a_scale)),
+                        from.a_at + static_cast<uint32_t>(offsetof(FewLds, w_scale)));
+  };
+  f32x4 acc[TM][kFewN] = {};
+  const int slot = (piece ^ (r & 7)) << 4;
+  const int a_frag = r * kBlock + slot, w_frag = (wave * 16 * kFewN + (r >> 2) * 4 * kFewN + (r & 3)) * kBlock + slot;
+  auto multiply = [&](int kb, int stage, auto tail, uint32_t left) {
+    union Piece {
+      u32x4 half[2];
+      i32x8 all;
+    };
+    auto read = [&](const uint8_t* side, int at) {
+      Piece u;
+      u.half[0] = *reinterpret_cast<const u32x4*>(side + at);
+      u.half[1] = *reinterpret_cast<const u32x4*>(side + (at ^ 64));
+      return u;
+    };
+    const float sw = lds.w_scale[wave * 16 * kFewN / kBlock][kb % kScaleBlocks];
+    Piece w[kFewN];
+#pragma unroll
+    for (int j = 0; j < kFewN; ++j) {
+      w[j] = read(&lds.w[stage][j * 4 * kBlock], w_frag);
+      if (decltype(tail)::value) {   // pieces behind the row's end
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if ((piece + 4 * h) * 16 >= left) w[j].half[h] = u32x4{0, 0, 0, 0};
+      }
+    }
+    const Op wo[kFewN] = {Op(w[0].all), Op(w[1].all)};
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const Op a(read(&lds.a[stage][i * 16 * kBlock], a_frag).all);
+      const float s = lds.a_scale[i * 16 + r][kb % kScaleBlocks] * sw;
+#pragma unroll
+      for (int j = 0; j < kFewN; ++j) {
+        const f32x4 p = mfma_block(wo[j], a);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(p[v], s, acc[i][j][v]);
+      }
+    }
+  };
+  const int full = g.K / kBlock, last = full - 1;
+  if (full > 0) {
+    for (int kb = 0; kb <= last; ++kb) {
+      if (kb % kScaleBlocks == 0) {
+        if (kb > 0) {   // every wavefront is through with the scales that are replaced
+          asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+          __builtin_amdgcn_s_barrier();
+        }
+        scales(kb);
+      }
+      // this block has landed (the later ones' loads may be in flight), and every wavefront is through
+      // with the stage that the one kFewStages - 1 later goes to
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"((kFewStages - 2) * kLoads) : "memory");
+      __builtin_amdgcn_s_barrier();
+      few_load(from, (kb + kFewStages - 1) % kFewStages, min(kb + kFewStages - 1, last) * kBlock);
+      multiply(kb, kb % kFewStages, std::false_type{}, kBlock);
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");   // the last stages' loads
+    __builtin_amdgcn_s_barrier();
+  }
+  // A short last block, not overlapped (see gemm_tile).
+  if (full < g.kb) {
+    const uint32_t left = g.K - full * kBlock;
+    if (full % kScaleBlocks == 0) scales(full);
+#pragma unroll
+    for (int q = 0; q < from.kW; ++q) from.load_w(q, 0, full * kBlock, from.w_chunk() < left ? 0 : -from.w_chunk());
+    from.load_a(0, 0, full * kBlock, from.a_chunk() < left ? 0 : -from.a_chunk());
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+    __builtin_amdgcn_s_barrier();
+    multiply(full, 0, std::true_type{}, left);
+    asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+    __builtin_amdgcn_s_barrier();
+  }
+  if (next.rows > 0) {
+    from.aim(g, next);
+    few_start(g, from);
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+    store_row<kFewN, DT>(g, tile, i * 16 + r, tile.col_tile * kTileN + wave * 16 * kFewN + piece * 4 * kFewN, acc[i]);
+}
+
+template <int DT>
+__global__ __launch_bounds__(kTileThreads, 2) void fp8_gemm_few_kernel(GemmArgs g, int col_tiles) {
+  __shared__ __align__(1024) FewLds lds;
+  const int row_tiles = count_row_tiles(g, kFewM);
+  const TileRun run = die_tiles(static_cast<uint32_t>(row_tiles) * col_tiles, blockIdx.x % 8);
+  uint32_t t = run.first + blockIdx.x / 8;
+  if (t >= run.end) return;
+  FewLoader from;
+  from.a_at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((MOE_LDS uint8_t*)&lds.a[0][0]));
+  from.w_at = from.a_at + static_cast<uint32_t>(offsetof(FewLds, w));
+  Tile tile = tile_at(g, kFewM, row_tiles, col_tiles, t);
+  from.aim(g, tile);
+  few_start(g, from);
+  while (tile.rows > 0) {
+    t += gridDim.x / 8;
+    Tile next{0, 0, 0, 0};
+    if (t < run.end) next = tile_at(g, kFewM, row_tiles, col_tiles, t);
+    if (tile.rows > 16) few_tile<2, DT>(g, tile, next, from, lds);
+    else few_tile<1, DT>(g, tile, next, from, lds);
+    tile = next;
+  }
+}
+
 // Workgroups for tiles of BM by BN: every group with rows may have one partly filled row tile.
 int tile_blocks(const GemmArgs& g, int BM, int BN, uint32_t* blocks, int* col_tiles) {
   *col_tiles = (g.N + BN - 1) / BN;
@@ -598,16 +749,51 @@ int tile_blocks(const GemmArgs& g, int BM, int BN, uint32_t* blocks, int* col_ti
   return MOE_OK;
 }
 
+// LDS holds one workgroup of the tile kernels per compute unit: each takes tiles until its die's run
+// is done.
+uint32_t resident_grid(uint32_t blocks) {
+  return min(blocks, static_cast<uint32_t>((device_cu_count() + 7) / 8 * 8));
+}
+
+// Rows of the highest tile: what finishes first when every compute unit takes its tiles in turn, from
+// the average group's rows.  A tile's time goes with its rows plus about 64 for the weights' part (777
+// rows by 11264 columns in fp32: 62 us with 96-row tiles, two rounds, against 70 us with 112-row
+// ones, two rounds as well, and 71 us with 64-row ones, three; 256 rows for each of 64 experts: 419 us
+// with 256-row tiles, 456 us with 128-row ones).
+int tile_rows(const GemmArgs& g, int most) {
+  const int groups = min(g.E, g.M), n = (g.M + groups - 1) / groups;
+  const int64_t cus = device_cu_count(), cols = static_cast<int64_t>(groups) * ((g.N + kTileN - 1) / kTileN);
+  int best = most;
+  int64_t least = INT64_MAX;
+  for (int bm = most; bm >= 64; bm -= 32) {
+    const int tiles = (n + bm - 1) / bm, high = ((n + tiles - 1) / tiles + 31) / 32 * 32;
+    const int64_t cost = (tiles * cols + cus - 1) / cus * (max(high, 64) + 64);
+    if (cost < least) {
+      least = cost;
+      best = bm;
+    }
+  }
+  return best;
+}
+
 template <int DT>
 int launch_tile(const GemmArgs& g, hipStream_t stream) {
   uint32_t blocks;
   int col_tiles;
-  const int bm = kTileM<DT>;
+  const int bm = tile_rows(g, kTileM<DT>);
   if (int rc = tile_blocks(g, bm, kTileN, &blocks, &col_tiles)) return rc;
-  // LDS holds one workgroup per compute unit: each takes tiles until its die's run is done
-  const uint32_t grid = min(blocks, static_cast<uint32_t>((device_cu_count() + 7) / 8 * 8));
   ProfileScope prof("fp8_gemm", stream);
-  hipLaunchKernelGGL(fp8_gemm_tile_kernel<DT>, dim3(grid), dim3(kTileThreads), 0, stream, g, bm, col_tiles);
+  hipLaunchKernelGGL(fp8_gemm_tile_kernel<DT>, dim3(resident_grid(blocks)), dim3(kTileThreads), 0, stream, g, bm, col_tiles);
+  return check_launch("fp8_gemm");
+}
+
+template <int DT>
+int launch_few(const GemmArgs& g, hipStream_t stream) {
+  uint32_t blocks;
+  int col_tiles;
+  if (int rc = tile_blocks(g, kFewM, kTileN, &blocks, &col_tiles)) return rc;
+  ProfileScope prof("fp8_gemm", stream);
+  hipLaunchKernelGGL(fp8_gemm_few_kernel<DT>, dim3(resident_grid(blocks)), dim3(kTileThreads), 0, stream, g, col_tiles);
   return check_launch("fp8_gemm");
 }
 
@@ -623,9 +809,16 @@ int launch_stream(const GemmArgs& g, hipStream_t stream) {
 
 template <int DT>
 int launch_gemm(const GemmArgs& g, hipStream_t stream) {
+  // More than 64 rows to a group on average: products bound it.
+  if (g.M > 64 * g.E) return launch_tile<DT>(g, stream);
+  // Fewer: the weights do.  From two 256-column tiles for each compute unit on the direct loads through
+  // LDS keep memory busiest (64 experts, 128 tokens, 1300 tiles: 204 us, against 319 us with the
+  // weights read into registers, 16 bytes to a cache access).  Below that the finer 32-column tiles of
+  // the register kernel fill the chip better (2 experts, 224 tiles: 46 us against 52 us).
+  const int64_t row_tiles = max(min(g.E, g.M), (g.M + kFewM - 1) / kFewM);
+  if (row_tiles * ((g.N + kTileN - 1) / kTileN) >= 2 * device_cu_count()) return launch_few<DT>(g, stream);
   if (g.M <= 16 * g.E) return launch_stream<1, 2, DT>(g, stream);
-  if (g.M <= 64 * g.E) return launch_stream<2, 2, DT>(g, stream);
-  return launch_tile<DT>(g, stream);
+  return launch_stream<2, 2, DT>(g, stream);
 }
 
 }  // namespace
