@@ -382,31 +382,38 @@ def moe_profile_stop(max_kernels: int = 32) -> dict:
 # ---------------------------------------------------------------------------------------------
 MOE_DTYPE_F16, MOE_DTYPE_BF16, MOE_DTYPE_F32 = 0, 1, 2
 MOE_FP8_BLOCK = 128
-_row_types = {}   # torch dtype -> MOE_DTYPE_* of row elements, and torch's own names; filled at the first call
+_ROW_DTYPES = {}   # torch dtype -> MOE_DTYPE_* of row elements, filled at the first call
+_torch = None      # what these calls use of torch; the module itself does not need it to be loaded
 
 
-def _types():
-    if not _row_types:
+class _Torch:
+    def __init__(self):
         import torch
-        _row_types.update({torch.float16: MOE_DTYPE_F16, torch.bfloat16: MOE_DTYPE_BF16,
-                           torch.float32: MOE_DTYPE_F32, "i32": torch.int32, "f32": torch.float32,
-                           "e4m3": (torch.float8_e4m3fn, torch.uint8),
-                           "device": torch.cuda.current_device, "on": torch.cuda.device,
-                           "stream": torch._C._cuda_getCurrentRawStream})
-    return _row_types
+        _ROW_DTYPES.update({torch.float16: MOE_DTYPE_F16, torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32})
+        self.i32, self.f32, self.e4m3 = torch.int32, torch.float32, (torch.float8_e4m3fn, torch.uint8)
+        self.device, self.stream, self.on = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, torch.cuda.device
+        # creates the context, as any CUDA tensor has done before
+        torch.cuda.current_device() if torch.cuda.is_available() else None
+
+
+def _loaded() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
 
 
 def _bad(fn: str, msg: str) -> MoeError:
     return MoeError(fn, MOE_EINVAL, msg)
 
 
-def _rows(fn: str, name: str, t, rows: int, cols: int, dtype, device) -> int:
-    """Check a [rows, cols] tensor with contiguous rows; returns its row stride in elements."""
-    if t.dtype is not dtype and t.dtype != dtype:
+def _rows(fn: str, name: str, t, rows: int, cols: int, dtype, device: int) -> int:
+    """Check a [rows, cols] tensor with contiguous rows on GPU `device`; returns its row stride."""
+    if t.dtype is not dtype:
         raise _bad(fn, f"{name} is {t.dtype}, not {dtype}")
-    if t.device != device:
-        raise _bad(fn, f"{name} is on {t.device}, not {device}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.get_device() != device:
+        raise _bad(fn, f"{name} is on {t.device}, not cuda:{device}")
+    if t.shape != (rows, cols):
         raise _bad(fn, f"{name} has shape {tuple(t.shape)}, not {(rows, cols)}")
     step, one = t.stride()
     if one != 1 and cols > 1:
@@ -414,20 +421,20 @@ def _rows(fn: str, name: str, t, rows: int, cols: int, dtype, device) -> int:
     return step if rows > 1 else max(step, cols)
 
 
-def _flat(fn: str, name: str, t, numel: int, dtype, device) -> int:
-    """Check a contiguous tensor of `numel` elements; returns its address."""
-    if t.dtype != dtype:
+def _whole(fn: str, name: str, t, shape, dtype, device: int) -> int:
+    """Check a contiguous tensor of `shape` on GPU `device`; returns its address."""
+    if t.dtype is not dtype:
         raise _bad(fn, f"{name} is {t.dtype}, not {dtype}")
-    if t.device != device:
-        raise _bad(fn, f"{name} is on {t.device}, not {device}")
-    if t.numel() != numel or not t.is_contiguous():
-        raise _bad(fn, f"{name} needs {numel} contiguous elements (shape {tuple(t.shape)}, strides {t.stride()})")
+    if t.get_device() != device:
+        raise _bad(fn, f"{name} is on {t.device}, not cuda:{device}")
+    if t.shape != shape or not t.is_contiguous():
+        raise _bad(fn, f"{name} needs shape {shape}, contiguous (has {tuple(t.shape)}, strides {t.stride()})")
     return t.data_ptr()
 
 
 def _row_dtype(fn: str, name: str, t) -> int:
-    ty = _types()
-    code = ty.get(t.dtype)
+    _torch or _loaded()
+    code = _ROW_DTYPES.get(t.dtype)
     if code is None:
         raise _bad(fn, f"{name} is {t.dtype}: rows are float16, bfloat16 or float32")
     if not t.is_cuda:
@@ -437,19 +444,16 @@ def _row_dtype(fn: str, name: str, t) -> int:
     return code
 
 
-def _run_on(fn: str, device, stream, *args) -> None:
-    """Call `fn` with the device of its tensors current, on `stream` or that device's current one."""
-    ty = _types()
-    index = device.index
-    call = getattr(_lib, fn)
+def _run_on(fn: str, call, device: int, stream, *args) -> None:
+    """Call with the device of its tensors current, on `stream` or that device's current one."""
     if stream is None:
-        handle = ty["stream"](index)
+        handle = _torch.stream(device)
     else:
         handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if index == ty["device"]():
+    if device == _torch.device():
         rc = call(*args, handle)
     else:
-        with ty["on"](index):
+        with _torch.on(device):
             rc = call(*args, handle)
     if rc != MOE_OK:
         _check(fn, rc)
@@ -460,93 +464,98 @@ def moe_permute_tokens(x, topk_ids, expert_offsets, sorted_pairs, x_sorted, pair
     (rows behind them are left alone), and pair_rows int32 [T, k], the row of each pair or -1.
     x [T, H] and x_sorted [T*k, H] fp16, bf16 or fp32 with contiguous rows."""
     fn = "moe_permute_tokens"
-    code, dev, i32 = _row_dtype(fn, "x", x), x.device, _types()["i32"]
+    code, dev = _row_dtype(fn, "x", x), x.get_device()
+    i32, dt = _torch.i32, x.dtype
     T, H = x.shape
-    k = topk_ids.shape[1] if topk_ids.dim() == 2 else topk_ids.numel() // max(T, 1)
-    n = T * k
-    _run_on(fn, dev, stream, x.data_ptr(), code, _rows(fn, "x", x, T, H, x.dtype, dev), T, k,
-            expert_offsets.numel() - 1, H, _flat(fn, "topk_ids", topk_ids, n, i32, dev),
-            _flat(fn, "expert_offsets", expert_offsets, expert_offsets.numel(), i32, dev),
-            _flat(fn, "sorted_pairs", sorted_pairs, n, i32, dev), x_sorted.data_ptr(),
-            _rows(fn, "x_sorted", x_sorted, n, H, x.dtype, dev), _flat(fn, "pair_rows", pair_rows, n, i32, dev))
+    k = _slots(fn, "topk_ids", topk_ids, T)
+    n, offsets = T * k, expert_offsets.numel()
+    _run_on(fn, _lib.moe_permute_tokens, dev, stream, x.data_ptr(), code, _rows(fn, "x", x, T, H, dt, dev), T, k,
+            offsets - 1, H, _whole(fn, "topk_ids", topk_ids, (T, k), i32, dev),
+            _whole(fn, "expert_offsets", expert_offsets, (offsets,), i32, dev),
+            _whole(fn, "sorted_pairs", sorted_pairs, (n,), i32, dev), x_sorted.data_ptr(),
+            _rows(fn, "x_sorted", x_sorted, n, H, dt, dev), _whole(fn, "pair_rows", pair_rows, (T, k), i32, dev))
+
+
+def _slots(fn: str, name: str, t, T: int) -> int:
+    if t.dim() != 2 or t.shape[0] != T:
+        raise _bad(fn, f"{name} has shape {tuple(t.shape)}, not ({T}, k)")
+    return t.shape[1]
 
 
 def moe_permute_tokens_backward(dx_sorted, pair_rows, dx, stream=None) -> None:
     """dx[t] = sum of dx_sorted's rows of token t's pairs (pair_rows int32 [T, k]; -1: no row)."""
     fn = "moe_permute_tokens_backward"
-    code, dev = _row_dtype(fn, "dx", dx), dx.device
+    code, dev = _row_dtype(fn, "dx", dx), dx.get_device()
+    dt = dx.dtype
     T, H = dx.shape
-    n = pair_rows.numel()
-    _run_on(fn, dev, stream, dx_sorted.data_ptr(), code, _rows(fn, "dx_sorted", dx_sorted, n, H, dx.dtype, dev), T,
-            _slots(fn, pair_rows, T), H, _flat(fn, "pair_rows", pair_rows, n, _types()["i32"], dev), dx.data_ptr(),
-            _rows(fn, "dx", dx, T, H, dx.dtype, dev))
-
-
-def _slots(fn: str, pair_rows, T: int) -> int:
-    if pair_rows.dim() != 2 or pair_rows.shape[0] != T:
-        raise _bad(fn, f"pair_rows has shape {tuple(pair_rows.shape)}, not ({T}, k)")
-    return pair_rows.shape[1]
+    k = _slots(fn, "pair_rows", pair_rows, T)
+    _run_on(fn, _lib.moe_permute_tokens_backward, dev, stream, dx_sorted.data_ptr(), code,
+            _rows(fn, "dx_sorted", dx_sorted, T * k, H, dt, dev), T, k, H,
+            _whole(fn, "pair_rows", pair_rows, (T, k), _torch.i32, dev), dx.data_ptr(), _rows(fn, "dx", dx, T, H, dt, dev))
 
 
 def moe_unpermute_tokens(y_sorted, pair_rows, gates, y, add=None, stream=None) -> None:
     """y[t] = sum_j gates[t, j] * y_sorted[pair_rows[t, j]] (+ add[t]); gates fp32 [T, k] or None (1)."""
     fn = "moe_unpermute_tokens"
-    code, dev, ty = _row_dtype(fn, "y", y), y.device, _types()
+    code, dev = _row_dtype(fn, "y", y), y.get_device()
+    dt = y.dtype
     T, H = y.shape
-    n = pair_rows.numel()
-    _run_on(fn, dev, stream, y_sorted.data_ptr(), code, _rows(fn, "y_sorted", y_sorted, n, H, y.dtype, dev), T,
-            _slots(fn, pair_rows, T), H, _flat(fn, "pair_rows", pair_rows, n, ty["i32"], dev),
-            None if gates is None else _flat(fn, "gates", gates, n, ty["f32"], dev),
-            None if add is None else add.data_ptr(), 0 if add is None else _rows(fn, "add", add, T, H, y.dtype, dev),
-            y.data_ptr(), _rows(fn, "y", y, T, H, y.dtype, dev))
+    k = _slots(fn, "pair_rows", pair_rows, T)
+    _run_on(fn, _lib.moe_unpermute_tokens, dev, stream, y_sorted.data_ptr(), code,
+            _rows(fn, "y_sorted", y_sorted, T * k, H, dt, dev), T, k, H,
+            _whole(fn, "pair_rows", pair_rows, (T, k), _torch.i32, dev),
+            None if gates is None else _whole(fn, "gates", gates, (T, k), _torch.f32, dev),
+            None if add is None else add.data_ptr(), 0 if add is None else _rows(fn, "add", add, T, H, dt, dev),
+            y.data_ptr(), _rows(fn, "y", y, T, H, dt, dev))
 
 
 def moe_unpermute_tokens_backward(dy, y_sorted, pair_rows, gates, dy_sorted, dgates, stream=None) -> None:
     """dy_sorted[pair_rows[t, j]] = gates[t, j] * dy[t] and dgates[t, j] = <dy[t], y_sorted[pair_rows[t, j]]>
     (0 without a row).  dy_sorted or dgates may be None; y_sorted may be None when dgates is."""
     fn = "moe_unpermute_tokens_backward"
-    code, dev, ty = _row_dtype(fn, "dy", dy), dy.device, _types()
+    code, dev = _row_dtype(fn, "dy", dy), dy.get_device()
+    dt = dy.dtype
     T, H = dy.shape
-    n = pair_rows.numel()
+    k = _slots(fn, "pair_rows", pair_rows, T)
 
     def rows(name, t):
-        return (None, 0) if t is None else (t.data_ptr(), _rows(fn, name, t, n, H, dy.dtype, dev))
+        return (None, 0) if t is None else (t.data_ptr(), _rows(fn, name, t, T * k, H, dt, dev))
 
-    _run_on(fn, dev, stream, dy.data_ptr(), code, _rows(fn, "dy", dy, T, H, dy.dtype, dev), *rows("y_sorted", y_sorted),
-            T, _slots(fn, pair_rows, T), H, _flat(fn, "pair_rows", pair_rows, n, ty["i32"], dev),
-            None if gates is None else _flat(fn, "gates", gates, n, ty["f32"], dev), *rows("dy_sorted", dy_sorted),
-            None if dgates is None else _flat(fn, "dgates", dgates, n, ty["f32"], dev))
-
-
-def _e4m3(fn: str, name: str, t, device):
-    if t.dtype not in _types()["e4m3"]:
-        raise _bad(fn, f"{name} is {t.dtype}, not float8_e4m3fn (or uint8 holding it)")
-    if t.device != device:
-        raise _bad(fn, f"{name} is on {t.device}, not {device}")
+    _run_on(fn, _lib.moe_unpermute_tokens_backward, dev, stream, dy.data_ptr(), code, _rows(fn, "dy", dy, T, H, dt, dev),
+            *rows("y_sorted", y_sorted), T, k, H, _whole(fn, "pair_rows", pair_rows, (T, k), _torch.i32, dev),
+            None if gates is None else _whole(fn, "gates", gates, (T, k), _torch.f32, dev),
+            *rows("dy_sorted", dy_sorted), None if dgates is None else _whole(fn, "dgates", dgates, (T, k), _torch.f32, dev))
 
 
-def _quantize(fn: str, x, K: int, q, scales, n_rows, stream) -> None:
-    code, dev, ty = _row_dtype(fn, "x", x), x.device, _types()
+def _e4m3(fn: str, name: str, t):
+    """The type of a tensor that holds e4m3 values."""
+    dt = t.dtype
+    if dt not in _torch.e4m3:
+        raise _bad(fn, f"{name} is {dt}, not float8_e4m3fn (or uint8 holding it)")
+    return dt
+
+
+def _quantize(fn: str, call, x, wide: int, q, scales, n_rows, stream) -> None:
+    if x.dim() == 2 and x.shape[1] % wide:
+        raise _bad(fn, f"x has {x.shape[1]} columns: gate and up halves are equally wide")
+    code, dev = _row_dtype(fn, "x", x), x.get_device()
     M, cols = x.shape
-    _e4m3(fn, "q", q, dev)
-    _run_on(fn, dev, stream, x.data_ptr(), code, _rows(fn, "x", x, M, cols, x.dtype, dev), M, K,
-            None if n_rows is None else _flat(fn, "n_rows", n_rows, 1, ty["i32"], dev), q.data_ptr(),
-            _rows(fn, "q", q, M, K, q.dtype, dev),
-            _flat(fn, "scales", scales, M * -(-K // MOE_FP8_BLOCK), ty["f32"], dev))
+    K = cols // wide
+    _run_on(fn, call, dev, stream, x.data_ptr(), code, _rows(fn, "x", x, M, cols, x.dtype, dev), M, K,
+            None if n_rows is None else _whole(fn, "n_rows", n_rows, (1,), _torch.i32, dev), q.data_ptr(),
+            _rows(fn, "q", q, M, K, _e4m3(fn, "q", q), dev),
+            _whole(fn, "scales", scales, (M, (K + MOE_FP8_BLOCK - 1) // MOE_FP8_BLOCK), _torch.f32, dev))
 
 
 def moe_fp8_quantize(x, q, scales, n_rows=None, stream=None) -> None:
     """x [M, K] -> q e4m3 [M, K] and scales fp32 [M, ceil(K/128)], one for each 128 columns of a
     row.  n_rows: optional device int32 [1]; rows from it on are left alone."""
-    _quantize("moe_fp8_quantize", x, x.shape[-1], q, scales, n_rows, stream)
+    _quantize("moe_fp8_quantize", _lib.moe_fp8_quantize, x, 1, q, scales, n_rows, stream)
 
 
 def moe_fp8_quantize_silu(x, q, scales, n_rows=None, stream=None) -> None:
     """moe_fp8_quantize of silu(x[:, :K]) * x[:, K:], x [M, 2K] (the output of a gate_up product)."""
-    fn = "moe_fp8_quantize_silu"
-    if x.shape[-1] % 2:
-        raise _bad(fn, f"x has {x.shape[-1]} columns: gate and up halves are equally wide")
-    _quantize(fn, x, x.shape[-1] // 2, q, scales, n_rows, stream)
+    _quantize("moe_fp8_quantize_silu", _lib.moe_fp8_quantize_silu, x, 2, q, scales, n_rows, stream)
 
 
 def moe_fp8_gemm(a, a_scales, w, w_scales, c, expert_offsets=None, sorted_pairs=None, k: int = 1,
@@ -554,24 +563,28 @@ def moe_fp8_gemm(a, a_scales, w, w_scales, c, expert_offsets=None, sorted_pairs=
     """c[i] = row (i, or sorted_pairs[i] // k) of a times the transposed weights of row i's expert.
 
     a e4m3 [R, K] with scales fp32 [R, ceil(K/128)]; w e4m3 [E, N, K] (or [N, K]) contiguous with
-    scales fp32 [E, ceil(N/128), ceil(K/128)]; c [M, N] fp16, bf16 or fp32.  expert_offsets int32
-    [E+1] gives the groups of c's rows (None: one group); rows of c behind the last group are left
-    alone.  See the header for the rules."""
+    scales fp32 [E, ceil(N/128), ceil(K/128)] (or without E); c [M, N] fp16, bf16 or fp32.
+    expert_offsets int32 [E+1] gives the groups of c's rows (None: one group); rows of c behind the
+    last group are left alone.  See the header for the rules."""
     fn = "moe_fp8_gemm"
-    code, dev, ty = _row_dtype(fn, "c", c), c.device, _types()
+    code, dev = _row_dtype(fn, "c", c), c.get_device()
+    f32, i32 = _torch.f32, _torch.i32
     M, N = c.shape
+    if a.dim() != 2 or w.dim() not in (2, 3):
+        raise _bad(fn, f"a [R, K] and w [E, N, K] or [N, K] (got {tuple(a.shape)} and {tuple(w.shape)})")
     R, K = a.shape
-    E = w.shape[0] if w.dim() == 3 else 1
-    kb = -(-K // MOE_FP8_BLOCK)
-    _e4m3(fn, "a", a, dev)
-    _e4m3(fn, "w", w, dev)
+    each = tuple(w.shape[:-2])    # (E,) or ()
+    E = each[0] if each else 1
+    nb, kb = (N + MOE_FP8_BLOCK - 1) // MOE_FP8_BLOCK, (K + MOE_FP8_BLOCK - 1) // MOE_FP8_BLOCK
+    blocks = (E, nb, kb) if w_scales.dim() == 3 else (*each, nb, kb)
     if expert_offsets is not None and expert_offsets.numel() != E + 1:
         raise _bad(fn, f"expert_offsets has {expert_offsets.numel()} entries for {E} experts")
-    _run_on(fn, dev, stream, a.data_ptr(), _rows(fn, "a", a, R, K, a.dtype, dev),
-            _flat(fn, "a_scales", a_scales, R * kb, ty["f32"], dev), R, _flat(fn, "w", w, E * N * K, w.dtype, dev),
-            _flat(fn, "w_scales", w_scales, E * -(-N // MOE_FP8_BLOCK) * kb, ty["f32"], dev), E, M, N, K,
-            None if expert_offsets is None else _flat(fn, "expert_offsets", expert_offsets, E + 1, ty["i32"], dev),
-            None if sorted_pairs is None else _flat(fn, "sorted_pairs", sorted_pairs, M, ty["i32"], dev), k,
+    _run_on(fn, _lib.moe_fp8_gemm, dev, stream, a.data_ptr(), _rows(fn, "a", a, R, K, _e4m3(fn, "a", a), dev),
+            _whole(fn, "a_scales", a_scales, (R, kb), f32, dev), R,
+            _whole(fn, "w", w, (*each, N, K), _e4m3(fn, "w", w), dev),
+            _whole(fn, "w_scales", w_scales, blocks, f32, dev), E, M, N, K,
+            None if expert_offsets is None else _whole(fn, "expert_offsets", expert_offsets, (E + 1,), i32, dev),
+            None if sorted_pairs is None else _whole(fn, "sorted_pairs", sorted_pairs, (M,), i32, dev), k,
             c.data_ptr(), code, _rows(fn, "c", c, M, N, c.dtype, dev))
 
 
