@@ -825,15 +825,22 @@ int launch_stream(const GemmArgs& g, hipStream_t stream) {
 
 template <int DT>
 int launch_gemm(const GemmArgs& g, hipStream_t stream) {
-  // More than 64 rows to a group on average: products bound it.
-  if (g.M > 64 * g.E) return launch_tile<DT>(g, stream);
-  // Fewer: the weights do.  From two 256-column tiles for each compute unit on the direct loads through
-  // LDS keep memory busiest (64 experts, 128 tokens, 1300 tiles: 204 us, against 319 us with the
-  // weights read into registers, 16 bytes to a cache access).  Below that the finer 32-column tiles of
-  // the register kernel fill the chip better (2 experts, 224 tiles: 46 us against 52 us).
-  const int64_t row_tiles = max(min(g.E, g.M), (g.M + kFewM - 1) / kFewM);
-  if (row_tiles * ((g.N + kTileN - 1) / kTileN) >= 2 * device_cu_count()) return launch_few<DT>(g, stream);
-  if (g.M <= 16 * g.E) return launch_stream<1, 2, DT>(g, stream);
+  // By the average group's rows n and the tiles there are (us, 64 experts of 5120 x 3584 bf16 results):
+  //   n          24    32    48    64    96
+  //   tile      241   236   244   249   263     products and the L2 path bound it
+  //   few       218   252   284   341   437     weights bound it; over 32 rows they are read again
+  //   stream    316   431   561   677   975     finest tiles, weights 16 bytes to a cache access
+  // The first two need tiles for the whole chip: 2 experts of 28672 x 4096 (224 tiles) take 52 us as
+  // few and 46 as stream, 64 rows by 4096 x 4096 (32 tiles) 20 and 13; with 256 rows there (128 tiles)
+  // 21 and 40, since the stream kernel reads the weights again for every 32 rows.
+  const int groups = min(g.E, g.M), n = (g.M + groups - 1) / groups, cus = device_cu_count();
+  const int64_t cols = static_cast<int64_t>(groups) * ((g.N + kTileN - 1) / kTileN);
+  if (n > 28 && (n + 63) / 64 * cols >= cus) return launch_tile<DT>(g, stream);
+  if (n > 96 || (n + kFewM - 1) / kFewM * cols >= 2 * cus) return launch_few<DT>(g, stream);
+  // 16-column tiles where 32-column ones are few: one row by 4096 x 4096 8.6 -> 6.3 us, two experts of
+  // 4096 x 14336 23.4 -> 20.3 us; with 2560 tiles (2048 x 1408, 16 tokens) 21.8 -> 24.0 us instead.
+  if (n <= 16 && static_cast<int64_t>(groups) * ((g.N + 31) / 32) < 2 * cus) return launch_stream<1, 1, DT>(g, stream);
+  if (n <= 16) return launch_stream<1, 2, DT>(g, stream);
   return launch_stream<2, 2, DT>(g, stream);
 }
 

@@ -45,16 +45,23 @@ __device__ __forceinline__ uint32_t row_max_u32(uint32_t v) {
   return max_dpp32<0x140>(v);
 }
 
-// silu(g) * u.  exp(-g) as 2^t with the rounding of t = -g log2(e) carried along, so that the
-// result is good to a few units in the last place for every g: without the correction the
-// relative error grows as |g| 2^-24.
+// silu(g) * u.  exp(-g) as 2^t with the rounding of t = -g log2(e) carried along (without it the
+// relative error grows as |g| 2^-24), and the quotient g / (1 + e) corrected once by its remainder:
+// v is as exact as with a library exp and a division, so no more values than with those land on the
+// other side of an e4m3 border (7e-5 of the values' norm on normal data, 1.1e-4 without the
+// correction).  Outside +-86 the exponential is held at its value there, 1 + e is finite, and the
+// quotient is g on one side and taken as 0 on the other.
 __device__ __forceinline__ float silu_gate(float g, float u) {
   constexpr float kLog2e = 1.44269504088896340736f, kLog2eLow = 1.92596299112661746887e-8f, kLn2 = 0.69314718055994530942f;
-  const float t = -g * kLog2e;
-  const float low = fmaf(-g, kLog2e, -t) + -g * kLog2eLow;
+  const float h = __builtin_amdgcn_fmed3f(g, -86.0f, 86.0f);
+  const float t = -h * kLog2e;
+  const float low = fmaf(-h, kLog2eLow, fmaf(-h, kLog2e, -t));
   float e = __builtin_amdgcn_exp2f(t);
-  e = fabsf(t) < 128.0f ? fmaf(e, low * kLn2, e) : e;
-  return g * __builtin_amdgcn_rcpf(1.0f + e) * u;
+  e = fmaf(e, low * kLn2, e);
+  const float d = 1.0f + e;
+  const float r = g < -86.0f ? 0.0f : __builtin_amdgcn_rcpf(d);
+  const float q = g * r;
+  return fmaf(fmaf(-d, q, g), r, q) * u;
 }
 
 // One wavefront per (row, 512 columns).

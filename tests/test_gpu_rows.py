@@ -376,6 +376,136 @@ def test_gemm(T, E, k, N, K, ty, gather, drop, repeat, integers):
             assert _worst(f64(c), want[:r.n], size[:r.n], top[:r.n], K, ty) <= 1
 
 
+# Sizes that fill the chip, so that each form of the product runs: tiles of few rows, tiles of many (of
+# every height), several tiles to a workgroup, more blocks of K than their scales are staged for, a
+# short last block behind them.  The reference is torch's float64 product on the device.
+BIG_GEMM_CASES = [  # T, E, k, N, K, type, gather, dropped share
+    (64, 64, 2, 2100, 528, "bf16", True, 0.0),       # few rows each, 576 tiles
+    (96, 8, 2, 16400, 3728, "f16", True, 0.1),       # 24 rows each, 29 whole blocks and a short one
+    (96, 8, 2, 16400, 400, "f32", False, 0.0),
+    (600, 2, 1, 8200, 400, "bf16", True, 0.0),       # about 300 rows each: two tiles of up to 160
+    (600, 2, 1, 8200, 400, "f32", True, 0.05),
+    (520, 1, 1, 8200, 3728, "bf16", False, 0.0),
+    (520, 1, 1, 8200, 3728, "f32", False, 0.0),
+    (1500, 6, 1, 5130, 128, "f16", True, 0.0),       # one block only; about 250 rows each
+    (700, 40, 2, 4100, 64, "bf16", False, 0.02),     # no whole block
+    (1900, 40, 3, 2050, 272, "bf16", True, 0.0),
+    (256, 1, 1, 4100, 640, "bf16", False, 0.0),      # 128 tiles of few rows
+    (1, 1, 1, 4100, 2064, "bf16", False, 0.0),       # 16-column tiles
+    (40, 1, 1, 4100, 528, "f32", False, 0.0),        # 32-row stream
+] + [(n, 1, 1, 8300, 272, "bf16", False, 0.0) for n in (64, 145, 257)] + [
+    (16 * n, 16, 1, 8200, 272, ty, True, 0.0) for n in (40, 70, 100, 125, 150, 180, 210, 245) for ty in ("bf16", "f32")]
+
+
+@pytest.mark.parametrize("T,E,k,N,K,ty,gather,drop", BIG_GEMM_CASES)
+def test_gemm_on_the_whole_chip(T, E, k, N, K, ty, gather, drop):
+    say(f"big gemm T={T} E={E} k={k} N={N} K={K} {ty} gather={gather} drop={drop}")
+    r = Routing(T, E, k, T + N, drop)
+    g = torch.Generator(device=DEV).manual_seed(T + N + K)
+    table = torch.from_numpy(oracle.e4m3_values()).to(DEV)
+    small = torch.nonzero((table.abs() <= 8) & (table == table.round())).view(-1).to(torch.uint8)
+
+    def codes(*shape):
+        return small[torch.randint(0, len(small), shape, device=DEV, generator=g)]
+
+    def scales(*shape):
+        return 2.0 ** torch.randint(-1, 2, shape, device=DEV, generator=g).float()
+
+    R, kb, nb = (T if gather else T * k), -(-K // 128), -(-N // 128)
+    a = torch.full((R, K + 16), 127, dtype=torch.uint8, device=DEV)[:, :K]
+    a.copy_(codes(R, K))
+    w, sa, sw = codes(E, N, K), scales(R, kb), scales(E, nb, kb)
+    outputs = []
+    for _ in range(2):
+        c = strided(T * k, N, TYPES[ty], 55.0, 3)
+        apq.moe_fp8_gemm(a, sa, w, sw, c, expert_offsets=r.offsets if E > 1 else None,
+                         sorted_pairs=r.pairs if gather else None, k=k)
+        outputs.append(c)
+    assert torch.equal(outputs[0], outputs[1])       # the same bits again
+    assert bool((c[r.n:] == 55.0).all()) and bool((c.as_strided((T * k, 3), (N + 3, 1), N) == 55.0).all())
+    source = (r.pairs[:r.n].long() // k) if gather else torch.arange(r.n, device=DEV)
+    spread = torch.arange(K, device=DEV) // 128
+    for e, rows in enumerate(r.groups):
+        if len(rows) == 0:
+            continue
+        src = source[rows.start:rows.stop]
+        ae = table[a[src].long()] * sa[src].double()[:, spread]
+        we = table[w[e].long()] * sw[e].double().repeat_interleave(128, 0)[:N][:, spread]
+        want = ae @ we.t().contiguous()
+        assert torch.equal(c[rows.start:rows.stop], want.to(TYPES[ty]))
+
+
+@pytest.mark.parametrize("ty", ["f16", "bf16", "f32"])
+def test_rows_that_start_at_an_odd_element(ty):
+    """Views one element into their memory: aligned to an element only."""
+    T, E, k, H = 9, 4, 2, 150
+    dt, r = TYPES[ty], Routing(T, E, k, 21, 0.1)
+    g = torch.Generator(device=DEV).manual_seed(3)
+
+    def odd(rows, cols, fill=None, dtype=dt):
+        t = torch.full((rows * (cols + 2) + 1,), 5.0 if fill is None else fill, dtype=dtype, device=DEV)
+        return t[1:].view(rows, cols + 2)[:, :cols]
+
+    x, ys = odd(T, H), odd(T * k, H)
+    x.copy_(torch.randn(T, H, device=DEV, generator=g))
+    ys.copy_(torch.randn(T * k, H, device=DEV, generator=g))
+    xs, rows = odd(T * k, H), torch.empty(T, k, dtype=torch.int32, device=DEV)
+    apq.moe_permute_tokens(x, r.ids, r.offsets, r.pairs, xs, rows)
+    assert torch.equal(xs[:r.n], x[dev(r.pairs_np // k).long()])
+    got, want = odd(T, H), torch.empty(T, H, dtype=dt, device=DEV)
+    apq.moe_unpermute_tokens(ys, rows, r.gates, got, add=x)
+    apq.moe_unpermute_tokens(ys.contiguous(), rows, r.gates, want, add=x.contiguous())
+    assert torch.equal(got, want)
+    dys, dys2 = odd(T * k, H), torch.full((T * k, H), 5.0, dtype=dt, device=DEV)
+    dg, dg2 = torch.empty(T, k, device=DEV), torch.empty(T, k, device=DEV)
+    apq.moe_unpermute_tokens_backward(x, ys, rows, r.gates, dys, dg)
+    apq.moe_unpermute_tokens_backward(x.contiguous(), ys.contiguous(), rows, r.gates, dys2, dg2)
+    assert torch.equal(dys, dys2) and torch.equal(dg, dg2)
+    q, q2 = odd(T, H, 0, torch.uint8), torch.empty(T, H, dtype=torch.uint8, device=DEV)
+    s, s2 = torch.empty(T, 2, device=DEV), torch.empty(T, 2, device=DEV)
+    apq.moe_fp8_quantize(x, q, s)
+    apq.moe_fp8_quantize(x.contiguous(), q2, s2)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    a, w = torch.zeros(T, 64, dtype=torch.uint8, device=DEV), torch.full((1, H, 64), 56, dtype=torch.uint8, device=DEV)
+    a[:, 0] = 56                                      # 1.0
+    c = odd(T, H)
+    apq.moe_fp8_gemm(a, torch.ones(T, 1, device=DEV), w, torch.ones(1, 2, 1, device=DEV), c)
+    assert bool((c == 1.0).all()) and bool((c.as_strided((T, 2), (H + 2, 1), c.storage_offset() + H) == 5.0).all())
+
+
+def test_far_rows_of_a_large_array():
+    """Sorted rows that lie more than 2^32 bytes (and 2^31 elements) into their array."""
+    T, k, E, H = 40000, 8, 8, 8192                    # 320000 rows of 16 KiB: 5.2 GB
+    ids = torch.arange(T * k, dtype=torch.int32, device=DEV).view(T, k) % E
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=DEV)
+    pairs = torch.empty(T * k, dtype=torch.int32, device=DEV)
+    apq.moe_group_by_expert(ids, E, offsets, pairs, torch.empty(E, dtype=torch.int32, device=DEV),
+                            torch.empty(1, dtype=torch.int32, device=DEV))
+    x = (torch.arange(T, device=DEV)[:, None] % 251 + torch.arange(H, device=DEV) % 5).half()
+    xs, rows = torch.empty(T * k, H, dtype=torch.float16, device=DEV), torch.empty(T, k, dtype=torch.int32, device=DEV)
+    apq.moe_permute_tokens(x, ids, offsets, pairs, xs, rows)
+    tail = slice(T * k - 500, T * k)
+    assert torch.equal(xs[tail], x[pairs[tail].long() // k])
+    dx = torch.empty_like(x)
+    apq.moe_permute_tokens_backward(xs, rows, dx)
+    assert torch.equal(dx, x * k)                     # sums up to 2040: exact in fp16
+    dys, dg = torch.empty_like(xs), torch.empty(T, k, device=DEV)
+    apq.moe_unpermute_tokens_backward(x, xs, rows, None, dys, dg)
+    assert torch.equal(dys[tail], xs[tail])
+    q, s = torch.empty(T * k, H, dtype=torch.uint8, device=DEV), torch.empty(T * k, H // 128, device=DEV)
+    apq.moe_fp8_quantize(xs, q, s)
+    q1, s1 = torch.empty(500, H, dtype=torch.uint8, device=DEV), torch.empty(500, H // 128, device=DEV)
+    apq.moe_fp8_quantize(xs[tail], q1, s1)
+    assert torch.equal(q[tail], q1) and torch.equal(s[tail], s1)
+    # rows of a and c behind 2^31 bytes, read in place
+    N = 8
+    w, sw = torch.full((N, H), 56, dtype=torch.uint8, device=DEV), torch.ones(1, H // 128, device=DEV)
+    c, c1 = torch.empty(T * k, N, device=DEV), torch.empty(500, N, device=DEV)
+    apq.moe_fp8_gemm(q, s, w, sw, c)
+    apq.moe_fp8_gemm(q1, s1, w, sw, c1)
+    assert torch.equal(c[tail], c1)
+
+
 @pytest.mark.parametrize("T", [2, 40, 700])
 def test_gemm_nan_stays_in_its_row(T):
     """NaN in one row of a and one row of w reaches that row and that column of its expert only."""
