@@ -475,10 +475,10 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
     const float sw = lds.w_scale[wn >> 1][kb % kScaleBlocks];
     auto read_a = [&](int i) { return read(&lds.a[stage][i * 16 * kBlock], a_frag).all; };
     i32x8 a[2];
-    float s[3];
+    float s[2], a_scale[2];
     f32x4 p[kLag + 1];
     a[0] = read_a(0);
-    s[0] = f[0] * sw;
+    a_scale[0] = f[0];
     std::conditional_t<kFine, Op, int> wide[kWaveN];
     if constexpr (kFine) {
 #pragma unroll
@@ -488,7 +488,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
     auto add = [&](int n) {
 #pragma unroll
       for (int v = 0; v < 4; ++v)
-        acc[n / kWaveN][n % kWaveN][v] = fmaf(p[n % (kLag + 1)][v], s[n / kWaveN % 3], acc[n / kWaveN][n % kWaveN][v]);
+        acc[n / kWaveN][n % kWaveN][v] = fmaf(p[n % (kLag + 1)][v], s[n / kWaveN & 1], acc[n / kWaveN][n % kWaveN][v]);
     };
 #pragma unroll
     for (int n = 0; n < kSteps; ++n) {
@@ -497,9 +497,10 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, const Tile& tile, c
         op = Op(a[i & 1]);
         if (i + 1 < TM) {
           a[(i + 1) & 1] = read_a(i + 1);
-          s[(i + 1) % 3] = f[(i + 1) * 16 * kScalePitch] * sw;
+          a_scale[(i + 1) & 1] = f[(i + 1) * 16 * kScalePitch];
         }
       }
+      if (j == kLag) s[i & 1] = a_scale[i & 1] * sw;   // first used for the product kLag back: this row step's first
       if constexpr (kFine)
         p[n % (kLag + 1)] = mfma_block(wide[j], op);
       else
