@@ -3,14 +3,16 @@
 //   c[i][n] = sum_b sa[r_i][b] sw[e][n/128][b] sum_{kk in block b} a[r_i][kk] w[e][n][kk]
 //
 // for the rows i of expert e's group, r_i = i or pairs[i] / k.  One 16x16x128 matrix instruction
-// covers one block of 16 weight rows and 16 rows of a: its fp32 result is exact up to fp32
-// accumulation, and is added to the fp32 accumulator with the product of the two scales, one FMA
-// per element and block.
+// covers one block of 16 weight rows and 16 rows of a; its result is added to the fp32 accumulator with
+// the product of the two scales, one FMA per element and block (half the instruction's own time, and
+// beside it: with four FMAs to a product two wavefronts per SIMD still reach 4.0 PFLOP/s).
 //
 // Operand layout.  The weights are the instruction's A side (rows), a its B side (columns), so a
 // lane's four results are four neighbouring columns n of one row i of c and its scale sa is one
 // value.  The order of the 128 products inside a block does not matter, so lane (r, g) = (l % 16,
 // l / 16) simply takes the 16-byte pieces g and g + 4 of its row's block on both sides.
+//
+// Three forms, chosen in launch_gemm: many rows to a group, few rows with many tiles, few with few.
 #include <cstddef>
 #include <type_traits>
 
@@ -43,8 +45,9 @@ struct GemmArgs {
 
 // ---- tiles of the groups ---------------------------------------------------------------------
 // The n rows of a group are cut into ceil(n / bm) tiles of equal height (rounded up to 16 rows), so
-// that no tile is nearly empty; a tile of c is (row tile, column tile), and all tiles are numbered group by group, inside a group column tile by column tile with the row
-// tiles of one column tile side by side (they share its weights).
+// that no tile is nearly empty; a tile of c is (row tile, column tile), and all tiles are numbered
+// group by group, inside a group column tile by column tile with the row tiles of one column tile side
+// by side (they share its weights).
 struct Tile {
   int e, first, rows, col_tile;     // rows <= 0: no tile
 };
@@ -188,8 +191,12 @@ __device__ __forceinline__ i32x8 load_pieces(const uint8_t* row, int kb, int K, 
 constexpr int kStreamThreads = 256;
 constexpr int kStreamWaves = kStreamThreads / 64;
 
-// Few rows: the weights go straight from memory into registers, the four wavefronts of a workgroup
-// take every fourth block of K and add their results up at the end.
+// ---- few rows, few tiles -----------------------------------------------------------------------
+// Tiles of 16 or 32 columns, so that small products still fill the chip: the weights go straight from
+// memory into registers, the four wavefronts of a workgroup take every fourth block of K and add their
+// results up at the end, in a fixed order.  Reading the weights bounds it (two experts of 28672 x 4096,
+// one row each: 44 us, 5.4 TB/s); neighbouring lanes hold different rows, so the vector cache takes an
+// access for every 16 bytes, which is what caps larger products in this form.
 template <int MT, int NT, int DT>
 __global__ __launch_bounds__(kStreamThreads) void fp8_gemm_stream_kernel(GemmArgs g, int col_tiles) {
   constexpr int BM = MT * 16, BN = NT * 16;
@@ -286,6 +293,10 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_gemm_stream_kernel(GemmArg
 // 256-row ones for the same products.  (Weights are not loaded straight into registers: a matrix
 // operand wants neighbouring lanes on different rows, and the vector cache then takes one access for
 // every 16 bytes instead of one for 64.)
+//
+// 64 experts of 5120 x 3584 with about 256 rows each: 416 us, 1.44 PFLOP/s (about 330 us without the loads,
+// 290 without the products: two stages overlap them only in part).  777 rows by 11264 x 2048 in fp32:
+// 60 us, 0.6 PFLOP/s.
 constexpr int kTileThreads = 512, kTileWaves = kTileThreads / 64;
 constexpr int kTileN = 256, kWaveN = 4;      // kWaveN: 16-column pieces of a wavefront
 // Rows of the highest tile.  Accumulators fill half the registers; widening to fp16 needs the rest
@@ -618,7 +629,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_gemm_tile_kernel(GemmArgs
 // ---- few rows to a group, many weights ----------------------------------------------------------
 // Tiles of up to 32 rows by 256 columns, each of the eight wavefronts all rows by 32 columns.  The
 // weights are read once and bound it, so the stages are small enough for kFewStages of them and the
-// loads run kFewStages - 1 blocks ahead.
+// loads run kFewStages - 1 blocks ahead.  64 experts of 5120 x 3584 with 16 rows each: 204 us, 5.8 TB/s of
+// the 6.35 a pure read reaches.
 constexpr int kFewM = 32, kFewStages = 4, kFewN = 2;
 
 struct FewLds {

@@ -36,7 +36,8 @@ __device__ __forceinline__ void copy_row(const char* src, char* dst, int bytes, 
 }
 
 // One wavefront per sorted position i (and per pair p = i for the pairs without an expert).  A token's
-// row is read k times, from the caches after the first.
+// row is read k times, from the caches after the first.  Short on latency: 16 tokens x 4 rows of 4 KiB
+// take 2.4 us, against 2.7 us by token.
 template <int SIZE>
 __global__ __launch_bounds__(kRowThreads) void permute_gather_kernel(
     const char* __restrict__ x, int64_t x_bytes, int pairs_n, int k, int E, int row_bytes,
@@ -55,7 +56,9 @@ __global__ __launch_bounds__(kRowThreads) void permute_gather_kernel(
 }
 
 // One workgroup per token: its row is read once and written to its k places.  Slot j's place is found
-// in its expert's part of `pairs`, which ascends, by bisection (k lanes at once).
+// in its expert's part of `pairs`, which ascends, by bisection (k lanes at once).  2048 tokens x 8 rows
+// of 7 KiB: 28.9 us (4.6 TB/s), 32.7 us by sorted position; 512 tokens: 8.4 and 9.2 us, 256: 6.4 and 5.0 us;
+// 8192 tokens x 2 rows of 8 KiB: 46.0 and 40.6 us.  Hence the switch.
 template <int SIZE>
 __global__ __launch_bounds__(kRowThreads) void permute_token_kernel(
     const char* __restrict__ x, int64_t x_bytes, int pairs_n, int k, int E, int row_bytes,
@@ -99,7 +102,9 @@ __global__ __launch_bounds__(kRowThreads) void permute_token_kernel(
   }
 }
 
-// One wavefront per (token, 64 vectors of its row).
+// One wavefront per (token, 64 vectors of its row): enough wavefronts for a single token's rows to be
+// spread over the chip, and k independent loads a lane.  8192 tokens x 8 rows of 7 KiB with an added
+// row: 96 us, 5.9 TB/s; 4099 x 10 rows of 8 KiB in fp32, ungated: 62 us, 6.0 TB/s.
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(
     const typename Elem<DT>::T* __restrict__ ys, int64_t ys_stride, int T, int k, int H, int chunks,
@@ -136,7 +141,8 @@ __global__ __launch_bounds__(kRowThreads) void combine_rows_kernel(
 }
 
 // One workgroup per token.  Its dy stays in registers, kGradVecs vectors a lane at a time, while its
-// rows go by once; the lanes' products are added in a fixed order.
+// rows go by once; the lanes' products are added in a fixed order.  4096 tokens x 8 rows of 7 KiB: 100 us,
+// 5.0 TB/s of reads and writes in equal parts (a copy: 4.8).
 constexpr int kGradVecs = 2;
 
 template <int DT>
