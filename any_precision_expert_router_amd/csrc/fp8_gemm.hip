@@ -118,6 +118,51 @@ __device__ __forceinline__ TileRun die_tiles(uint32_t tiles, uint32_t die) {
   return {die * per, min((die + 1) * per, tiles)};
 }
 
+// The same, dealt out by what the tiles cost instead of by their number, for tiles of different
+// heights: in units of rows, a tile's own (in steps of 32, at least 64) plus 64 for the weights' part.
+// Groups of 250 and of 260 rows differ by one 256-row tile against two of 144; by number, the dies that
+// got the former had the longer run (64 experts, about 256 rows each: 428 us, 411 us by cost).
+__device__ __forceinline__ int tile_cost(int n, int tiles) {
+  return tiles > 0 ? max((tile_height(n, tiles) + 31) / 32 * 32, 64) + 64 : 0;
+}
+
+__device__ __forceinline__ int cost_row_tiles(const GemmArgs& g, int bm) {
+  const int lane = threadIdx.x & 63;
+  int total = 0;
+  for (int e0 = 0; e0 < g.E; e0 += 64) {
+    int first;
+    const int n = group_rows(g, e0 + lane, first), mt = (n + bm - 1) / bm;
+    total += lane_int(wave_inclusive_add(dpp_settled(mt * tile_cost(n, mt))), 63);
+  }
+  return total;
+}
+
+// First tile of die d's run; `cost` is cost_row_tiles().
+__device__ __forceinline__ uint32_t die_start(const GemmArgs& g, int bm, int row_tiles, int cost, int col_tiles, int d) {
+  const uint32_t tiles = static_cast<uint32_t>(row_tiles) * col_tiles;
+  if (d >= 8) return tiles;
+  if (!g.offsets) return static_cast<uint32_t>(static_cast<uint64_t>(tiles) * d / 8);
+  const uint64_t target = static_cast<uint64_t>(cost) * col_tiles * d / 8;
+  const int lane = threadIdx.x & 63;
+  int tiles_before = 0, cost_before = 0;
+  for (int e0 = 0; e0 < g.E; e0 += 64) {
+    int first;
+    const int n = group_rows(g, e0 + lane, first), mt = (n + bm - 1) / bm, each = tile_cost(n, mt);
+    const int cost_upto = wave_inclusive_add(dpp_settled(mt * each)), upto = wave_inclusive_add(dpp_settled(mt));
+    const int cost_all = cost_before + lane_int(cost_upto, 63);
+    if (static_cast<uint64_t>(cost_all) * col_tiles > target) {
+      const uint64_t hit = __ballot(static_cast<uint64_t>(cost_before + cost_upto) * col_tiles > target);
+      const int l = __builtin_ctzll(hit), mt_l = lane_int(mt, l), each_l = lane_int(each, l);
+      const uint64_t in = target - static_cast<uint64_t>(cost_before + lane_int(cost_upto, l) - mt_l * each_l) * col_tiles;
+      return static_cast<uint32_t>(tiles_before + lane_int(upto, l) - mt_l) * col_tiles +
+             static_cast<uint32_t>(in / static_cast<uint32_t>(each_l));
+    }
+    tiles_before += lane_int(upto, 63);
+    cost_before = cost_all;
+  }
+  return tiles;
+}
+
 // Row of a behind row i of c.
 __device__ __forceinline__ int64_t source_row(const GemmArgs& g, int i) {
   int r = i;
@@ -294,7 +339,7 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_gemm_stream_kernel(GemmArg
 // operand wants neighbouring lanes on different rows, and the vector cache then takes one access for
 // every 16 bytes instead of one for 64.)
 //
-// 64 experts of 5120 x 3584 with about 256 rows each: 416 us, 1.44 PFLOP/s (about 330 us without the loads,
+// 64 experts of 5120 x 3584 with about 256 rows each: 411 us, 1.46 PFLOP/s (about 330 us without the loads,
 // 290 without the products: two stages overlap them only in part).  777 rows by 11264 x 2048 in fp32:
 // 60 us, 0.6 PFLOP/s.
 constexpr int kTileThreads = 512, kTileWaves = kTileThreads / 64;
@@ -600,7 +645,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_gemm_tile_kernel(GemmArgs
   constexpr int BM = kTileM<DT>;
   __shared__ __align__(1024) TileLds<BM> lds;
   const int row_tiles = count_row_tiles(g, bm);
-  const TileRun run = die_tiles(static_cast<uint32_t>(row_tiles) * col_tiles, blockIdx.x % 8);
+  const int die = blockIdx.x % 8, cost = g.offsets ? cost_row_tiles(g, bm) : 0;
+  const TileRun run{die_start(g, bm, row_tiles, cost, col_tiles, die), die_start(g, bm, row_tiles, cost, col_tiles, die + 1)};
   uint32_t t = run.first + blockIdx.x / 8;
   if (t >= run.end) return;
   Loader<BM, kWaveN> from;

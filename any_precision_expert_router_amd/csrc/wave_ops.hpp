@@ -49,6 +49,10 @@ __device__ __forceinline__ float dpp_settled(float v) {
   asm volatile("s_nop 4" : "+v"(v));
   return v;
 }
+__device__ __forceinline__ int dpp_settled(int v) {
+  asm volatile("s_nop 4" : "+v"(v));
+  return v;
+}
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t max_dpp32(uint32_t v) {

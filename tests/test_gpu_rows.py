@@ -435,6 +435,45 @@ def test_gemm_on_the_whole_chip(T, E, k, N, K, ty, gather, drop):
         assert torch.equal(c[rows.start:rows.stop], want.to(TYPES[ty]))
 
 
+@pytest.mark.parametrize("T,E,N,K,ty", [(300, 64, 300, 272, "bf16"), (700, 512, 700, 400, "f32"), (5000, 16, 2600, 144, "f16")])
+def test_gemm_when_one_expert_takes_all(T, E, N, K, ty):
+    """Far more rows in one group than the average the launch goes by."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    ids = torch.full((T, 1), E - 2, dtype=torch.int32, device=DEV)
+    ids[5], ids[T // 2] = 0, E - 1
+    offsets, pairs = torch.empty(E + 1, dtype=torch.int32, device=DEV), torch.empty(T, dtype=torch.int32, device=DEV)
+    apq.moe_group_by_expert(ids, E, offsets, pairs, torch.empty(E, dtype=torch.int32, device=DEV),
+                            torch.empty(1, dtype=torch.int32, device=DEV))
+    table = torch.from_numpy(oracle.e4m3_values()).to(DEV)
+    small = torch.nonzero((table.abs() <= 8) & (table == table.round())).view(-1).to(torch.uint8)
+    a = small[torch.randint(0, len(small), (T, K), device=DEV, generator=g)]
+    w = small[torch.randint(0, len(small), (E, N, K), device=DEV, generator=g)]
+    sa, sw = torch.ones(T, -(-K // 128), device=DEV), torch.ones(E, -(-N // 128), -(-K // 128), device=DEV)
+    c = torch.empty(T, N, dtype=TYPES[ty], device=DEV)
+    apq.moe_fp8_gemm(a, sa, w, sw, c, expert_offsets=offsets, sorted_pairs=pairs, k=1)
+    order = pairs.long()
+    for rows in (slice(0, 1), slice(1, T - 1), slice(T - 1, T)):
+        e = int(ids[order[rows.start], 0])
+        want = table[a[order[rows]].long()] @ table[w[e].long()].t().contiguous()
+        assert torch.equal(c[rows], want.to(TYPES[ty]))
+
+
+def test_gemm_gathers_without_groups():
+    """sorted_pairs without expert_offsets: one group whose rows come from anywhere, some twice."""
+    g = torch.Generator(device=DEV).manual_seed(2)
+    for M, R, k, N, K in [(3, 2, 4, 40, 144), (50, 30, 2, 70, 256), (600, 90, 8, 8200, 272)]:
+        pairs = torch.randint(0, R * k, (M,), dtype=torch.int32, device=DEV, generator=g)
+        a = torch.randint(0, 80, (R, K), dtype=torch.uint8, device=DEV, generator=g)
+        w = torch.randint(0, 80, (N, K), dtype=torch.uint8, device=DEV, generator=g)
+        sa, sw = torch.ones(R, -(-K // 128), device=DEV), torch.ones(-(-N // 128), -(-K // 128), device=DEV)
+        c = torch.empty(M, N, device=DEV)
+        apq.moe_fp8_gemm(a, sa, w, sw, c, sorted_pairs=pairs, k=k)
+        table = torch.from_numpy(oracle.e4m3_values()).to(DEV)
+        want = (table[a.long()] @ table[w.long()].t().contiguous())[pairs.long() // k]
+        size = (table[a.long()].abs() @ table[w.long()].abs().t().contiguous())[pairs.long() // k]
+        assert bool(((c - want).abs() <= 2 * (K + 8) * U * size + U * want.abs()).all())
+
+
 @pytest.mark.parametrize("ty", ["f16", "bf16", "f32"])
 def test_rows_that_start_at_an_odd_element(ty):
     """Views one element into their memory: aligned to an element only."""
