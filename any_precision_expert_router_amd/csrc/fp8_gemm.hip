@@ -341,13 +341,13 @@ __global__ __launch_bounds__(kStreamThreads) void fp8_gemm_stream_kernel(GemmArg
 //
 // 64 experts of 5120 x 3584 with about 256 rows each: 411 us, 1.46 PFLOP/s (about 330 us without the loads,
 // 290 without the products: two stages overlap them only in part).  777 rows by 11264 x 2048 in fp32:
-// 60 us, 0.6 PFLOP/s.
+// 48 us, 0.75 PFLOP/s.
 constexpr int kTileThreads = 512, kTileWaves = kTileThreads / 64;
 constexpr int kTileN = 256, kWaveN = 4;      // kWaveN: 16-column pieces of a wavefront
 // Rows of the highest tile.  Accumulators fill half the registers; widening to fp16 needs the rest
 // for the weights.
 template <int DT>
-constexpr int kTileM = DT == MOE_DTYPE_F32 ? 128 : 256;
+constexpr int kTileM = DT == MOE_DTYPE_F32 ? 160 : 256;
 
 #define MOE_LDS __attribute__((address_space(3)))
 
@@ -418,7 +418,7 @@ struct Loader {
   }
   // Direct load q of a stage, from column `uniform` + `more` on.
   __device__ __forceinline__ void load_a(int q, int stage, uint32_t uniform, uint32_t more = 0) const {
-    const int part = (q * kTileWaves + wave()) % (BM / 8);   // few rows: some parts twice, the same bytes
+    const int part = (q * kTileWaves + wave()) % (BM / 8);   // some parts twice, the same bytes, if BM is not 64 n
     lds_load16(a_at + stage * (BM * kBlock) + part * 1024, a_rsrc, a_off[q] + more, uniform);
   }
   __device__ __forceinline__ void load_w(int q, int stage, uint32_t uniform, uint32_t more = 0) const {
@@ -659,15 +659,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void fp8_gemm_tile_kernel(GemmArgs
     t += gridDim.x / 8;
     Tile next{0, 0, 0, 0};
     if (t < run.end) next = tile_at(g, bm, row_tiles, col_tiles, t);
-    if constexpr (BM > 128) {
+    if constexpr (BM >= 256) {
       if (tile.rows > 224) gemm_tile<8, DT>(g, tile, next, from, lds);
       else if (tile.rows > 192) gemm_tile<7, DT>(g, tile, next, from, lds);
       else if (tile.rows > 160) gemm_tile<6, DT>(g, tile, next, from, lds);
-      else if (tile.rows > 128) gemm_tile<5, DT>(g, tile, next, from, lds);
     }
     if (tile.rows <= 64) gemm_tile<2, DT>(g, tile, next, from, lds);
     else if (tile.rows <= 96) gemm_tile<3, DT>(g, tile, next, from, lds);
     else if (tile.rows <= 128) gemm_tile<4, DT>(g, tile, next, from, lds);
+    else if (tile.rows <= 160) gemm_tile<5, DT>(g, tile, next, from, lds);
     tile = next;
   }
 }
@@ -832,9 +832,9 @@ uint32_t resident_grid(uint32_t blocks) {
 
 // Rows of the highest tile: what finishes first when every compute unit takes its tiles in turn, from
 // the average group's rows.  A tile's time goes with its rows plus about 64 for the weights' part (777
-// rows by 11264 columns in fp32: 62 us with 96-row tiles, two rounds, against 70 us with 112-row
-// ones, two rounds as well, and 71 us with 64-row ones, three; 256 rows for each of 64 experts: 419 us
-// with 256-row tiles, 456 us with 128-row ones).
+// rows by 11264 columns in fp32: 48 us with 160-row tiles, one round, 60 us with 96-row ones, two, 70
+// us with 112-row ones, two as well, and 71 us with 64-row ones, three; 256 rows for each of 64 experts:
+// 419 us with 256-row tiles, 456 us with 128-row ones).
 int tile_rows(const GemmArgs& g, int most) {
   const int groups = min(g.E, g.M), n = (g.M + groups - 1) / groups;
   const int64_t cus = device_cu_count(), cols = static_cast<int64_t>(groups) * ((g.N + kTileN - 1) / kTileN);
