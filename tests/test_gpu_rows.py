@@ -729,6 +729,42 @@ def test_two_runs_at_once_on_two_streams():
     assert _same(a.outputs(), want[0]) and _same(b.outputs(), want[1])
 
 
+def test_large_runs_captured_and_at_once():
+    """Sizes at which tokens are permuted by token and the products take whole tiles: captured and
+    replayed on changed inputs, and two different runs at once on two streams."""
+    a, b = Ffn(600, 8, 4, 512, 2048, 5), Ffn(900, 8, 4, 512, 2048, 6)
+    want = []
+    for f in (a, b):
+        f.run()
+        torch.cuda.synchronize()
+        want.append(f.outputs())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for f in (a, b):
+            for t in (f.y, f.o, f.h, f.xs):
+                t.zero_()
+        torch.cuda.synchronize()
+        for f, s in zip((a, b), streams):
+            f.run(stream=s)
+        torch.cuda.synchronize()
+        assert _same(a.outputs(), want[0]) and _same(b.outputs(), want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.run()
+    logits = a.logits.clone()
+    for turn in range(3):
+        a.logits.copy_(logits.flip(1) if turn % 2 else logits)
+        a.run()
+        torch.cuda.synchronize()
+        eager = a.outputs()
+        for t in (a.y, a.o, a.h, a.xs):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert _same(a.outputs(), eager)
+        assert _same(a.outputs(), want[0]) == (turn % 2 == 0)
+
+
 def test_binding_refuses_shapes_and_types():
     T, E, k, H = 4, 8, 2, 64
     r = Routing(T, E, k, 1)
